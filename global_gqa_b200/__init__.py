@@ -56,6 +56,17 @@ _SIGS = {
                                      _f32, _f32, _i32, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
     "g3attn_decode_no_alloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, ctypes.c_int,
                                               _i32, _f32, _f32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "g3attn_page_map": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                       _vp, _vp, _vp]),
+    "g3attn_paged_append": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _f32, _f32, _i32,
+                                           _i32, _i32, _i32, _vp, _vp, _vp]),
+    "g3attn_page_bounds": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "g3attn_page_select_workspace_size": (_sz, [_i32] * 3),
+    "g3attn_page_select": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
+                                          _vp, _sz, _vp, _vp]),
+    "g3attn_paged_decode_workspace_size": (_sz, [_i32] * 2),
+    "g3attn_paged_decode": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, ctypes.c_int, _i32, _i32, _i32, _i32,
+                                           _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "g3attn_check_device_error": (ctypes.c_int, [_vp, _vp]),
     "g3attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "g3attn_last_error": (ctypes.c_char_p, []),
@@ -445,3 +456,226 @@ def soft_tokens(patches, gamma, grid_h: int, grid_w: int, pool: int = 4, *, out=
                                       _stream_ptr(stream, dev))
     _check(st, "g3attn_soft_tokens")
     return out
+
+
+# ------------------------------------------------------------- paged cache
+# A decode step makes several of these calls per layer, each a few microseconds
+# on the GPU: arguments that are right pass one short test each, the messages
+# come from the checks above only when one is not.
+_paged_statuses = {}
+
+
+def paged_status(device=None):
+    """The device's error words of the paged calls (int32 [2]), used where no `status` is given.
+
+    Read and cleared by check_device_error(paged_status(device)).  Made on first
+    use, which must be outside a stream capture.
+    """
+    torch = _torch()
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    st = _paged_statuses.get(dev.index)
+    if st is None:
+        with torch.cuda.device(dev):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("call paged_status() once before capturing paged calls, or give them a status")
+            st = torch.zeros(2, dtype=torch.int32, device=dev)
+            torch.cuda.current_stream(dev).synchronize()  # any stream may use it from now on
+        st = _paged_statuses.setdefault(dev.index, st)
+    return st
+
+
+def _arg(t, name, dtype, shape, device) -> int:
+    """The address of a tensor argument; raises unless it is contiguous, of this type and shape, on this GPU."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _req(t, name, dtype, shape)
+    _on_device(device, **{name: t})
+    raise ValueError(f"{name} is not usable")
+
+
+def _dims(t, name, dtype, n: int):
+    """The shape of a leading argument, checked on its own."""
+    _req(t, name, dtype)
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _paged_call(fn, device, stream, status, *args) -> None:
+    """One library call on `device`'s stream, with the status words and the stream appended."""
+    torch = _torch()
+    if status is None:
+        status = _paged_statuses.get(device.index)
+        if status is None:
+            status = paged_status(device)
+    st = _arg(status, "status", torch.int32, (2,), device)
+    if torch.cuda.current_device() == device.index:
+        code = getattr(lib(), fn)(*args, st, _stream_ptr(stream, device))
+    else:
+        with torch.cuda.device(device):
+            code = getattr(lib(), fn)(*args, st, _stream_ptr(stream, device))
+    if code != 0:
+        _check(code, fn)
+
+
+def _empty(stream, device, shape, dtype):
+    """An output or workspace whose memory belongs to the stream that the call runs on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _stream_ptr(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def page_select_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
+    return int(lib().g3attn_page_select_workspace_size(B, Hkv, max_pages))
+
+
+def paged_decode_workspace_size(B: int, D: int) -> int:
+    return int(lib().g3attn_paged_decode_workspace_size(B, D))
+
+
+def page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size: int, n_pages: int, max_tokens: int, *,
+             out=None, status=None, stream=None):
+    """Block table entries (in place), slots and positions of one step's new tokens.
+
+    old_lens, new_lens int32 [B] (tokens cached, tokens added), block_table int32
+    [B, max_pages], free_pages int32 [capacity] (a ring of free page numbers),
+    free_state int32 [2] (its head and count).  Returns dict(seq_lens [B],
+    cu_tokens [B+1], slots [max_tokens], positions [max_tokens], free_state [2]),
+    all int32; `out` may hold preallocated ones under the same keys.
+    """
+    torch = _torch()
+    i32 = torch.int32
+    B, = _dims(old_lens, "old_lens", i32, 1)
+    _, max_pages = _dims(block_table, "block_table", i32, 2)
+    dev = old_lens.device
+    cap, = _dims(free_pages, "free_pages", i32, 1)
+    r = dict(out) if out is not None else {}
+    for name, n in (("seq_lens", B), ("cu_tokens", B + 1), ("slots", max_tokens), ("positions", max_tokens),
+                    ("free_state", 2)):
+        if name not in r:
+            r[name] = _empty(stream, dev, (n,), i32)
+    _paged_call("g3attn_page_map", dev, stream, status, old_lens.data_ptr(), _arg(new_lens, "new_lens", i32, (B,), dev), B,
+                _arg(block_table, "block_table", i32, (B, max_pages), dev), max_pages,
+                _arg(free_pages, "free_pages", i32, (cap,), dev), cap, _arg(free_state, "free_state", i32, (2,), dev),
+                page_size, n_pages, max_tokens, _arg(r["seq_lens"], "seq_lens", i32, (B,), dev),
+                _arg(r["cu_tokens"], "cu_tokens", i32, (B + 1,), dev), _arg(r["slots"], "slots", i32, (max_tokens,), dev),
+                _arg(r["positions"], "positions", i32, (max_tokens,), dev),
+                _arg(r["free_state"], "out free_state", i32, (2,), dev))
+    return r
+
+
+def paged_append(k, v, k_gamma, positions, slots, k_pages, v_pages, rope_base: float, interp_factor: float, *, q=None,
+                 q_gamma=None, q_hat=None, status=None, stream=None):
+    """QK-norm and RoPE of T packed tokens: keys and values into their slots; returns q_hat (None without q).
+
+    k, v bf16 [T,Hkv,D] and q bf16 [T,Hq,D] raw projections, gammas fp32 [D],
+    positions and slots int32 [T] (slot below 0: not cached), k_pages/v_pages bf16
+    [n_pages,Hkv,page_size,D] (updated in place).
+    """
+    torch = _torch()
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T, Hkv, D = _dims(k, "k", bf16, 3)
+    pool = _dims(k_pages, "k_pages", bf16, 4)
+    n_pages, _, P, _ = pool
+    dev = k.device
+    Hq, pq, pg, ph = 0, None, None, None
+    if q is not None:
+        Hq = _dims(q, "q", bf16, 3)[1]
+        if q_hat is None:
+            q_hat = _empty(stream, dev, (T, Hq, D), bf16)
+        pq, pg = _arg(q, "q", bf16, (T, Hq, D), dev), _arg(q_gamma, "q_gamma", f32, (D,), dev)
+        ph = _arg(q_hat, "q_hat", bf16, (T, Hq, D), dev)
+    elif q_gamma is not None or q_hat is not None:
+        raise ValueError("q_gamma and q_hat are given with q only")
+    _paged_call("g3attn_paged_append", dev, stream, status, pq, k.data_ptr(), _arg(v, "v", bf16, (T, Hkv, D), dev), pg,
+                _arg(k_gamma, "k_gamma", f32, (D,), dev), _arg(positions, "positions", i32, (T,), dev),
+                _arg(slots, "slots", i32, (T,), dev), _arg(k_pages, "k_pages", bf16, (n_pages, Hkv, P, D), dev),
+                _arg(v_pages, "v_pages", bf16, (n_pages, Hkv, P, D), dev), n_pages, P, rope_base, interp_factor, T, Hq,
+                Hkv, D, ph)
+    return q_hat
+
+
+def page_bounds(k_pages, block_table, old_lens, seq_lens, bounds, exps, *, status=None, stream=None):
+    """Renews the key bounds of the pages that hold tokens old_lens .. seq_lens-1; returns (bounds, exps).
+
+    k_pages bf16 [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages],
+    old_lens/seq_lens int32 [B]; bounds int8 [n_pages,Hkv,2,D] and exps int8
+    [n_pages,Hkv], updated in place.
+    """
+    torch = _torch()
+    i32, i8 = torch.int32, torch.int8
+    n_pages, Hkv, P, D = _dims(k_pages, "k_pages", torch.bfloat16, 4)
+    B, max_pages = _dims(block_table, "block_table", i32, 2)
+    dev = k_pages.device
+    _paged_call("g3attn_page_bounds", dev, stream, status, k_pages.data_ptr(),
+                _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(old_lens, "old_lens", i32, (B,), dev),
+                _arg(seq_lens, "seq_lens", i32, (B,), dev), B, max_pages, n_pages, P, Hkv, D,
+                _arg(bounds, "bounds", i8, (n_pages, Hkv, 2, D), dev), _arg(exps, "exps", i8, (n_pages, Hkv), dev))
+    return bounds, exps
+
+
+def page_select(q_hat, bounds, exps, block_table, seq_lens, page_size: int, n_select: int, *, out=None, ws=None,
+                status=None, stream=None):
+    """The newest page and the n_select-1 best-scored others of each (sequence, kv head), ascending, -1 behind.
+
+    q_hat bf16 [B,Hq,D] from paged_append, bounds/exps from page_bounds; returns
+    int32 [B,Hkv,n_select], for paged_decode(pages=...).
+    """
+    torch = _torch()
+    i32, i8 = torch.int32, torch.int8
+    B, Hq, D = _dims(q_hat, "q_hat", torch.bfloat16, 3)
+    n_pages, Hkv = _dims(exps, "exps", i8, 2)
+    _, max_pages = _dims(block_table, "block_table", i32, 2)
+    dev = q_hat.device
+    if out is None:
+        out = _empty(stream, dev, (B, Hkv, max(n_select, 0)), i32)
+    if ws is None:
+        ws = _empty(stream, dev, (max(page_select_workspace_size(B, Hkv, max_pages), 1),), torch.uint8)
+    ws, ws_bytes = _ws(ws, 0, dev)
+    _paged_call("g3attn_page_select", dev, stream, status, q_hat.data_ptr(),
+                _arg(bounds, "bounds", i8, (n_pages, Hkv, 2, D), dev), _arg(exps, "exps", i8, (n_pages, Hkv), dev),
+                _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), B,
+                max_pages, n_pages, page_size, Hq, Hkv, D, n_select, _arg(out, "out", i32, (B, Hkv, n_select), dev),
+                ws.data_ptr(), ws_bytes)
+    return out
+
+
+def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int, window: int, *, pages=None, out=None,
+                 return_lse: bool = False, ws=None, status=None, stream=None):
+    """Attention of one new token per sequence over its pages; returns out [B,Hq,D] (and lse [B,Hq]).
+
+    q_hat bf16 [B,Hq,D] from paged_append, k_pages/v_pages bf16
+    [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages], seq_lens int32 [B]
+    (the new token included; 0: idle, a zero row), pages int32 [B,Hkv,n] from
+    page_select or None (all pages; the last `window` tokens on a LOCAL layer).
+    """
+    torch = _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
+    B, Hq, D = _dims(q_hat, "q_hat", bf16, 3)
+    n_pages, Hkv, P, _ = _dims(k_pages, "k_pages", bf16, 4)
+    _, max_pages = _dims(block_table, "block_table", i32, 2)
+    dev = q_hat.device
+    pool = (n_pages, Hkv, P, D)
+    n_select, plist = 0, None
+    if pages is not None:
+        n_select = _dims(pages, "pages", i32, 3)[2]
+        plist = _arg(pages, "pages", i32, (B, Hkv, n_select), dev)
+    if out is None:
+        out = _empty(stream, dev, (B, Hq, D), bf16)
+    lse = _empty(stream, dev, (B, Hq), torch.float32) if return_lse else None
+    if ws is None:
+        ws = _empty(stream, dev, (max(paged_decode_workspace_size(B, D), 1),), torch.uint8)
+    ws, ws_bytes = _ws(ws, 0, dev)
+    _paged_call("g3attn_paged_decode", dev, stream, status, q_hat.data_ptr(), _arg(k_pages, "k_pages", bf16, pool, dev),
+                _arg(v_pages, "v_pages", bf16, pool, dev), _arg(block_table, "block_table", i32, (B, max_pages), dev),
+                _arg(seq_lens, "seq_lens", i32, (B,), dev), plist, n_select, int(layer_kind), int(window), B, max_pages,
+                n_pages, P, Hq, Hkv, D, _arg(out, "out", bf16, (B, Hq, D), dev), _ptr(lse), ws.data_ptr(), ws_bytes)
+    return (out, lse) if return_lse else out

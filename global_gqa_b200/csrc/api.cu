@@ -821,6 +821,293 @@ g3_status g3attn_soft_tokens(const void* patches, const float* gamma, int32_t B,
   return G3_OK;
 }
 
+// -------------------------------------------------------------- paged cache
+static int page_shift_of(int32_t page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+// What the calls on a pool of pages have in common; D = 0 where no rows are touched.
+static g3_status check_pool(const char* who, int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size, int32_t Hkv,
+                            int32_t D) {
+  if (B < 1 || max_pages < 1 || n_pages < 1 || Hkv < 1 || D < 0)
+    return fail(G3_ERR_INVALID_ARG, "%s: sizes must be positive (B=%d max_pages=%d n_pages=%d Hkv=%d D=%d)", who, B,
+                max_pages, n_pages, Hkv, D);
+  if (page_shift_of(page_size) < 0)
+    return fail(G3_ERR_UNSUPPORTED, "%s: page_size %d not built (16, 32, 64, 128, 256)", who, page_size);
+  if (D != 0 && !supported_d(D)) return fail(G3_ERR_UNSUPPORTED, "%s: head_dim %d not built (64, 128, 256)", who, D);
+  if (B > g3::kPagedMaxSeqs)
+    return fail(G3_ERR_UNSUPPORTED, "%s: B=%d sequences, at most %d are built", who, B, g3::kPagedMaxSeqs);
+  if ((long long)n_pages * page_size > 0x7fffffffLL)
+    return fail(G3_ERR_UNSUPPORTED, "%s: %d pages of %d tokens: slots must fit in 31 bits", who, n_pages, page_size);
+  if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)B * max_pages * (page_size / 16) > 0x7fffffffLL)
+    return fail(G3_ERR_UNSUPPORTED, "%s: a block table of %d x %d pages is too large", who, B, max_pages);
+  if (Hkv > 0xffff) return fail(G3_ERR_UNSUPPORTED, "%s: Hkv=%d too large", who, Hkv);
+  return G3_OK;
+}
+static g3_status check_group(const char* who, int32_t Hq, int32_t Hkv) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return fail(G3_ERR_INVALID_ARG, "%s: Hq %% Hkv != 0 (%d, %d)", who, Hq, Hkv);
+  if (Hq / Hkv > 8) return fail(G3_ERR_UNSUPPORTED, "%s: group size %d not built (1 to 8)", who, Hq / Hkv);
+  return G3_OK;
+}
+
+g3_status g3attn_page_map(const int32_t* old_lens, const int32_t* new_lens, int32_t B, int32_t* block_table,
+                          int32_t max_pages, const int32_t* free_pages, int32_t free_capacity,
+                          const int32_t* free_state, int32_t page_size, int32_t n_pages, int32_t max_tokens,
+                          int32_t* seq_lens, int32_t* cu_tokens, int32_t* slots, int32_t* positions,
+                          int32_t* free_state_out, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (!old_lens || !new_lens || !block_table || !free_pages || !free_state || !seq_lens || !cu_tokens || !slots ||
+      !positions || !free_state_out)
+    return fail(G3_ERR_INVALID_ARG, "page_map: a required pointer is NULL");
+  if (free_capacity < 1 || max_tokens < 1 || max_tokens == 0x7fffffff)
+    return fail(G3_ERR_INVALID_ARG, "page_map: bad free_capacity %d or max_tokens %d", free_capacity, max_tokens);
+  const g3_status s = check_pool("page_map", B, max_pages, n_pages, page_size, 1, 0);
+  if (s != G3_OK) return s;
+  // Every block reads all inputs while others write: no output may lie on an input or on another output.
+  const struct { const void* p; size_t n; } in[] = {{old_lens, (size_t)B * 4}, {new_lens, (size_t)B * 4},
+                                                    {free_pages, (size_t)free_capacity * 4}, {free_state, 8}},
+      out[] = {{block_table, (size_t)B * max_pages * 4}, {seq_lens, (size_t)B * 4}, {cu_tokens, (size_t)B * 4 + 4},
+               {slots, (size_t)max_tokens * 4}, {positions, (size_t)max_tokens * 4}, {free_state_out, 8}};
+  for (int i = 0; i < 6; ++i) {
+    for (const auto& x : in)
+      if (overlap(out[i].p, out[i].n, x.p, x.n)) return fail(G3_ERR_INVALID_ARG, "page_map: an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(G3_ERR_INVALID_ARG, "page_map: two outputs overlap");
+  }
+  g3::PageMapParams p{};
+  p.old_lens = old_lens;
+  p.new_lens = new_lens;
+  p.block_table = block_table;
+  p.free_pages = free_pages;
+  p.free_state = free_state;
+  p.seq_lens = seq_lens;
+  p.cu_tokens = cu_tokens;
+  p.slots = slots;
+  p.positions = positions;
+  p.free_state_out = free_state_out;
+  p.status = status;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.free_cap = free_capacity;
+  p.page_size = page_size;
+  p.page_shift = page_shift_of(page_size);
+  p.n_pages = n_pages;
+  p.max_tokens = max_tokens;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = traced("page_map", st, [&] { return g3::launch_page_map(p, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_map: %s", cudaGetErrorString(e));
+  return G3_OK;
+}
+
+g3_status g3attn_paged_append(const void* q, const void* k, const void* v, const float* q_gamma, const float* k_gamma,
+                              const int32_t* positions, const int32_t* slots, void* k_pages, void* v_pages,
+                              int32_t n_pages, int32_t page_size, float rope_base, float interp_factor, int32_t T,
+                              int32_t Hq, int32_t Hkv, int32_t D, void* q_hat, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (T < 0) return fail(G3_ERR_INVALID_ARG, "paged_append: T=%d", T);
+  if (!(rope_base > 0.f) || !std::isfinite(rope_base)) return fail(G3_ERR_INVALID_ARG, "paged_append: bad rope_base");
+  if (!(interp_factor > 0.f) || !std::isfinite(interp_factor))
+    return fail(G3_ERR_INVALID_ARG, "paged_append: bad interp_factor");
+  if ((Hq == 0) != (q == nullptr && q_gamma == nullptr && q_hat == nullptr) || Hq < 0 ||
+      (Hq > 0 && T > 0 && (!q || !q_gamma || !q_hat)))
+    return fail(G3_ERR_INVALID_ARG, "paged_append: give q, q_gamma and q_hat with Hq > 0, or none of them with Hq = 0");
+  const g3_status s = check_pool("paged_append", 1, 1, n_pages, page_size, Hkv, D < 1 ? -1 : D);
+  if (s != G3_OK) return s;
+  if (T == 0) return G3_OK;
+  if (!k || !v || !k_gamma || !positions || !slots || !k_pages || !v_pages)
+    return fail(G3_ERR_INVALID_ARG, "paged_append: a required pointer is NULL");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_hat) || !aligned16(k_pages) || !aligned16(v_pages))
+    return fail(G3_ERR_INVALID_ARG, "paged_append: q, k, v, q_hat and the pages must be 16-byte aligned");
+  if ((long long)Hq + Hkv > 0xffff) return fail(G3_ERR_UNSUPPORTED, "paged_append: Hq=%d too large", Hq);
+  g3::PagedAppendParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_gamma = q_gamma;
+  p.k_gamma = k_gamma;
+  p.positions = positions;
+  p.slots = slots;
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.q_hat = static_cast<__nv_bfloat16*>(q_hat);
+  p.status = status;
+  p.interp = interp_factor;
+  for (int f = 0; f < D / 2; ++f) p.inv_freq[f] = std::exp(-2.0 * f / D * std::log((double)rope_base));
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.page_shift = page_shift_of(page_size);
+  p.n_slots = n_pages * page_size;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = traced("paged_append", st, [&] { return g3::launch_paged_append(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "paged_append: %s", cudaGetErrorString(e));
+  return G3_OK;
+}
+
+g3_status g3attn_page_bounds(const void* k_pages, const int32_t* block_table, const int32_t* old_lens,
+                             const int32_t* seq_lens, int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                             int32_t Hkv, int32_t D, int8_t* bounds, int8_t* exps, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (!k_pages || !block_table || !old_lens || !seq_lens || !bounds || !exps)
+    return fail(G3_ERR_INVALID_ARG, "page_bounds: a required pointer is NULL");
+  const g3_status s = check_pool("page_bounds", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
+  if (s != G3_OK) return s;
+  if (!aligned16(k_pages) || !aligned16(bounds))
+    return fail(G3_ERR_INVALID_ARG, "page_bounds: k_pages and bounds must be 16-byte aligned");
+  g3::PageBoundsParams p{};
+  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  p.block_table = block_table;
+  p.old_lens = old_lens;
+  p.seq_lens = seq_lens;
+  p.bounds = bounds;
+  p.exps = exps;
+  p.status = status;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.Hkv = Hkv;
+  p.page_shift = page_shift_of(page_size);
+  p.n_pages = n_pages;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = traced("page_bounds", st, [&] { return g3::launch_page_bounds(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_bounds: %s", cudaGetErrorString(e));
+  return G3_OK;
+}
+
+size_t g3attn_page_select_workspace_size(int32_t B, int32_t Hkv, int32_t max_pages) {
+  if (B < 1 || Hkv < 1 || max_pages < 1) return 0;
+  return align_up((size_t)B * Hkv * max_pages * 4, 256);
+}
+
+g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8_t* exps, const int32_t* block_table,
+                             const int32_t* seq_lens, int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                             int32_t Hq, int32_t Hkv, int32_t D, int32_t n_select, int32_t* pages, void* workspace,
+                             size_t workspace_bytes, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (!q_hat || !bounds || !exps || !block_table || !seq_lens || !pages)
+    return fail(G3_ERR_INVALID_ARG, "page_select: a required pointer is NULL");
+  if (n_select < 1) return fail(G3_ERR_INVALID_ARG, "page_select: n_select=%d", n_select);
+  g3_status s = check_pool("page_select", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
+  if (s == G3_OK) s = check_group("page_select", Hq, Hkv);
+  if (s != G3_OK) return s;
+  if (!aligned16(q_hat) || !aligned16(bounds))
+    return fail(G3_ERR_INVALID_ARG, "page_select: q_hat and bounds must be 16-byte aligned");
+  const size_t need = g3attn_page_select_workspace_size(B, Hkv, max_pages);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(G3_ERR_WORKSPACE, "page_select: workspace NULL or not 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(G3_ERR_WORKSPACE, "page_select: workspace %zu bytes < required %zu", workspace_bytes, need);
+  g3::PageSelectParams p{};
+  p.q_hat = static_cast<const __nv_bfloat16*>(q_hat);
+  p.bounds = bounds;
+  p.exps = exps;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.scores = static_cast<float*>(workspace);
+  p.pages = pages;
+  p.status = status;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.page_shift = page_shift_of(page_size);
+  p.n_pages = n_pages;
+  p.n_select = n_select;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced("page_scores", st, [&] { return g3::launch_page_scores(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_select scores: %s", cudaGetErrorString(e));
+  e = traced("page_pick", st, [&] { return g3::launch_page_pick(p, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_select pick: %s", cudaGetErrorString(e));
+  return G3_OK;
+}
+
+namespace {
+struct PagedDecodeWs {
+  size_t pref, part_ml, part_o, total;
+};
+PagedDecodeWs paged_decode_ws(int B, int D) {
+  PagedDecodeWs w;
+  const size_t slots = 2 * (size_t)g3::paged_decode_blocks(D);
+  w.pref = 0;
+  w.part_ml = align_up(((size_t)B + 1) * 4, 256);
+  w.part_o = align_up(w.part_ml + slots * 8 * 2 * 4, 256);
+  w.total = w.part_o + slots * 8 * D * 4;
+  return w;
+}
+}  // namespace
+
+size_t g3attn_paged_decode_workspace_size(int32_t B, int32_t D) {
+  if (B < 1 || B > g3::kPagedMaxSeqs || !supported_d(D)) return 0;
+  return paged_decode_ws(B, D).total;
+}
+
+g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* pages, int32_t n_select, g3_layer_kind layer_kind,
+                              int32_t window, int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                              int32_t Hq, int32_t Hkv, int32_t D, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (!q_hat || !k_pages || !v_pages || !block_table || !seq_lens || !out)
+    return fail(G3_ERR_INVALID_ARG, "paged_decode: a required pointer is NULL");
+  if (layer_kind != G3_LAYER_LOCAL && layer_kind != G3_LAYER_GLOBAL)
+    return fail(G3_ERR_INVALID_ARG, "paged_decode: bad layer kind %d", (int)layer_kind);
+  if (layer_kind == G3_LAYER_LOCAL && window < 1) return fail(G3_ERR_INVALID_ARG, "paged_decode: window < 1");
+  if ((pages == nullptr) != (n_select == 0) || n_select < 0)
+    return fail(G3_ERR_INVALID_ARG, "paged_decode: pages must be NULL iff n_select == 0");
+  if (pages != nullptr && layer_kind != G3_LAYER_GLOBAL)
+    return fail(G3_ERR_UNSUPPORTED, "paged_decode: a page list is for global layers (a local one has its window)");
+  g3_status s = check_pool("paged_decode", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
+  if (s == G3_OK) s = check_group("paged_decode", Hq, Hkv);
+  if (s != G3_OK) return s;
+  if ((long long)B * std::min(n_select, max_pages) * (page_size / 16) > 0x7fffffffLL)
+    return fail(G3_ERR_UNSUPPORTED, "paged_decode: too many selected pages");
+  if (!aligned16(q_hat) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+    return fail(G3_ERR_INVALID_ARG, "paged_decode: q_hat, the pages and out must be 16-byte aligned");
+  const PagedDecodeWs w = paged_decode_ws(B, D);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(G3_ERR_WORKSPACE, "paged_decode: workspace NULL or not 256-byte aligned");
+  if (workspace_bytes < w.total)
+    return fail(G3_ERR_WORKSPACE, "paged_decode: workspace %zu bytes < required %zu", workspace_bytes, w.total);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  g3::PagedDecodeParams p{};
+  p.q_hat = static_cast<const __nv_bfloat16*>(q_hat);
+  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.pages = pages;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = status;
+  p.pref = reinterpret_cast<int32_t*>(ws + w.pref);
+  p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  p.B = B;
+  p.max_pages = max_pages;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.page_shift = page_shift_of(page_size);
+  p.n_pages = n_pages;
+  p.n_select = n_select;
+  p.kind = (int)layer_kind;
+  p.window = window;
+  p.n_blocks = g3::paged_decode_blocks(D);
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced("paged_decode", st, [&] { return g3::launch_paged_decode(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "paged_decode: %s", cudaGetErrorString(e));
+  e = traced("paged_combine", st, [&] { return g3::launch_paged_combine(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "paged_decode combine: %s", cudaGetErrorString(e));
+  return G3_OK;
+}
+
 g3_status g3attn_check_device_error(void* workspace, void* stream) {
   if (workspace == nullptr) return fail(G3_ERR_WORKSPACE, "check: workspace is NULL");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

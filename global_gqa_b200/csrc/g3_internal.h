@@ -183,4 +183,89 @@ cudaError_t launch_decode_prologue(const DecodeParams& p, int D, cudaStream_t st
 cudaError_t launch_decode_split(const DecodeParams& p, int D, int grid_chunks, cudaStream_t st);
 cudaError_t launch_decode_combine(const DecodeParams& p, int D, cudaStream_t st);
 
+// ------------------------------------------------------------- paged cache
+// k_pages, v_pages [n_pages, Hkv, P, D], P = 1 << page_shift in 16 .. 256.
+constexpr int kPagedMaxSeqs = 8192;  // sequences of one call: every block keeps a prefix sum over them in shared memory
+struct PageMapParams {
+  const int32_t* old_lens;    // [B]
+  const int32_t* new_lens;    // [B]
+  int32_t* block_table;       // [B, max_pages]
+  const int32_t* free_pages;  // [free_cap] ring
+  const int32_t* free_state;  // [2] head, count
+  int32_t* seq_lens;          // [B]
+  int32_t* cu_tokens;         // [B + 1]
+  int32_t* slots;             // [max_tokens]
+  int32_t* positions;         // [max_tokens]
+  int32_t* free_state_out;    // [2]
+  int* status;                // [2] or null
+  int B, max_pages, free_cap, page_size, page_shift, n_pages, max_tokens;
+};
+cudaError_t launch_page_map(const PageMapParams& p, cudaStream_t st);
+
+struct PagedAppendParams {
+  const __nv_bfloat16* q;  // [T, Hq, D]; Hq = 0: none
+  const __nv_bfloat16* k;  // [T, Hkv, D]
+  const __nv_bfloat16* v;
+  const float* q_gamma;
+  const float* k_gamma;
+  const int32_t* positions;  // [T]
+  const int32_t* slots;      // [T], below 0: not cached
+  __nv_bfloat16* k_pages;
+  __nv_bfloat16* v_pages;
+  __nv_bfloat16* q_hat;  // [T, Hq, D]
+  int* status;
+  double interp;
+  double inv_freq[128];  // base^(-2f/D), f < D/2
+  int T, Hq, Hkv, page_shift, n_slots;
+  int warps_per_token;  // set by the launcher
+};
+cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st);
+
+struct PageBoundsParams {
+  const __nv_bfloat16* k_pages;
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* old_lens;     // [B]
+  const int32_t* seq_lens;     // [B]
+  int8_t* bounds;              // [n_pages, Hkv, 2, D]: largest, smallest
+  int8_t* exps;                // [n_pages, Hkv]
+  int* status;
+  int B, max_pages, Hkv, page_shift, n_pages;
+};
+cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st);
+
+struct PageSelectParams {
+  const __nv_bfloat16* q_hat;  // [B, Hq, D]
+  const int8_t* bounds;
+  const int8_t* exps;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  float* scores;   // [B, Hkv, max_pages]
+  int32_t* pages;  // [B, Hkv, n_select]
+  int* status;
+  int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select;
+};
+cudaError_t launch_page_scores(const PageSelectParams& p, int D, cudaStream_t st);
+cudaError_t launch_page_pick(const PageSelectParams& p, cudaStream_t st);
+
+struct PagedDecodeParams {
+  const __nv_bfloat16* q_hat;  // [B, Hq, D]
+  const __nv_bfloat16* k_pages;
+  const __nv_bfloat16* v_pages;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* pages;  // [B, Hkv, n_select] or null
+  __nv_bfloat16* out;    // [B, Hq, D]
+  float* lse;            // [B, Hq] or null
+  int* status;
+  int32_t* pref;   // [B + 1]: units before each sequence, from the decode kernel to the combine
+  float* part_ml;  // [2 * n_blocks, 8, 2] (max, sum) in log2 units
+  float* part_o;   // [2 * n_blocks, 8, D]
+  int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select, kind, window;
+  int n_blocks;
+  float scale_log2;
+};
+int paged_decode_blocks(int D);
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, int D, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedDecodeParams& p, int D, cudaStream_t st);
+
 }  // namespace g3

@@ -1,0 +1,708 @@
+// Paged KV cache: the page map, the append of new tokens, the pages' key bounds
+// and the selection of pages by a score on those bounds.  (The attention over
+// the pages is in paged_decode.cu.)
+//
+//   page_map      : block tables, slots and positions of a step's new tokens
+//                   from the requests' lengths and a ring of free pages.
+//   paged_append  : QK-RMSNorm + RoPE of packed tokens; keys and values go to
+//                   their slots, queries to a packed buffer.
+//   page_bounds   : feature-wise largest and smallest key of each page and kv
+//                   head, in 8 bits.
+//   page_scores   : an upper bound of q . k over each page's keys, from the bounds.
+//   page_pick     : the pages with the highest scores of each (sequence, kv head).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "func_attr.cuh"
+#include "g3_internal.h"
+#include "paged_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace g3 {
+
+// ================================================================= page map
+// Integer work of a few kilobytes: bound by launch and latency.  Every block
+// scans all requests into shared memory (so blocks need no order among them)
+// and then takes its share of the tokens and of the new table entries.
+constexpr int kMapThreads = 1024;
+constexpr int kMapTokensPerBlock = 2 * kMapThreads;
+
+// Sums of non-negative terms that stop at `cap`: associative, and 32 bits are
+// enough for any lengths (cap < 2^31).
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap) { return min(a + b, cap); }
+
+__global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) {
+  extern __shared__ int map_smem[];
+  uint32_t* ends = reinterpret_cast<uint32_t*>(map_smem);  // [B] rows up to and with request b (stops at max_tokens + 1)
+  int* cum = map_smem + p.B;                               // [B] pages asked for up to and with request b
+  __shared__ uint32_t s_rows[32];
+  __shared__ int s_need[32];
+  __shared__ int s_taken;
+  griddep_wait();
+  griddep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t cap = (uint32_t)p.max_tokens + 1u;
+  const long long room = (long long)p.max_pages * p.page_size;
+  int head = p.free_state[0], count = p.free_state[1];
+  const bool ring_ok = head >= 0 && head < p.free_cap && count >= 0 && count <= p.free_cap;
+  if (!ring_ok) {
+    head = 0;
+    count = 0;
+  }
+  if (tid == 0) s_taken = 0;
+
+  // Rows first: whether a request fits the token buffer decides whether it asks for pages.
+  uint32_t rows_before = 0;
+  int need_before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kMapThreads) {
+    const int b = b0 + tid;
+    int old_len = 0, new_len = 0;
+    if (b < p.B) {
+      old_len = p.old_lens[b];
+      new_len = p.new_lens[b];
+    }
+    uint32_t rows = min((uint32_t)max(new_len, 0), cap);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, rows, off);
+      if (lane >= off) rows = sat_add(rows, v, cap);
+    }
+    if (lane == 31) s_rows[warp] = rows;
+    __syncthreads();
+    uint32_t add = rows_before;
+    for (int w = 0; w < warp; ++w) add = sat_add(add, s_rows[w], cap);
+    rows = sat_add(rows, add, cap);
+    for (int w = 0; w < kMapThreads / 32; ++w) rows_before = sat_add(rows_before, s_rows[w], cap);
+
+    const bool valid = b < p.B && old_len >= 0 && new_len >= 0 && (long long)old_len + new_len <= room && rows < cap;
+    const int have = valid ? (old_len + p.page_size - 1) >> p.page_shift : 0;
+    const int need = valid ? (int)(((long long)old_len + new_len + p.page_size - 1) >> p.page_shift) - have : 0;
+    int c = need;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, c, off);
+      if (lane >= off) c += v;
+    }
+    if (lane == 31) s_need[warp] = c;
+    __syncthreads();
+    c += need_before;
+    for (int w = 0; w < warp; ++w) c += s_need[w];
+    for (int w = 0; w < kMapThreads / 32; ++w) need_before += s_need[w];
+    if (b < p.B) {
+      ends[b] = rows;
+      cum[b] = c;
+      const bool granted = valid && (need == 0 || c <= count);
+      if (granted && need > 0) atomicMax(&s_taken, c);
+      if (blockIdx.x == 0) {
+        p.seq_lens[b] = granted ? old_len + new_len : (old_len >= 0 && old_len <= room ? old_len : 0);
+        p.cu_tokens[b + 1] = (int)min(rows, (uint32_t)p.max_tokens);
+        if (b == 0) p.cu_tokens[0] = 0;
+        if (!valid) record_error(p.status, kErrInvalid, 300);
+        if (valid && !granted) record_error(p.status, kErrInvalid, 301);
+      }
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    p.free_state_out[0] = (int)(((long long)head + s_taken) % p.free_cap);
+    p.free_state_out[1] = count - s_taken;
+    if (!ring_ok) record_error(p.status, kErrInvalid, 303);
+  }
+
+  // A granted request's fresh page i (0-based among its own) or -1.
+  auto fresh_page = [&](int asked_before, int i) {
+    const int id = p.free_pages[((long long)head + asked_before + i) % p.free_cap];
+    return id >= 0 && id < p.n_pages ? id : -1;
+  };
+
+  // New table entries: one warp per request.
+  for (int b = blockIdx.x * (kMapThreads / 32) + warp; b < p.B; b += gridDim.x * (kMapThreads / 32)) {
+    const int asked = b > 0 ? cum[b - 1] : 0, need = cum[b] - asked;
+    if (need == 0 || cum[b] > count) continue;
+    const int have = (p.old_lens[b] + p.page_size - 1) >> p.page_shift;
+    for (int i = lane; i < need; i += 32) {
+      const int id = fresh_page(asked, i);
+      p.block_table[(size_t)b * p.max_pages + have + i] = id;
+      if (id < 0) record_error(p.status, kErrInvalid, 302);
+    }
+  }
+
+  // Slot and position of every row of the token buffer.
+  for (int t = blockIdx.x * kMapThreads + tid; t < p.max_tokens; t += gridDim.x * kMapThreads) {
+    int slot = -1, pos = 0;
+    if ((uint32_t)t < ends[p.B - 1]) {
+      int lo = -1, hi = p.B - 1;  // ends[lo] <= t < ends[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] <= (uint32_t)t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int b = hi, old_len = p.old_lens[b], new_len = p.new_lens[b];
+      const int asked = b > 0 ? cum[b - 1] : 0, need = cum[b] - asked;
+      const bool valid = old_len >= 0 && new_len >= 0 && (long long)old_len + new_len <= room && ends[b] < cap;
+      if (valid && (need == 0 || cum[b] <= count)) {
+        pos = old_len + t - (b > 0 ? (int)ends[b - 1] : 0);
+        const int j = pos >> p.page_shift, have = (old_len + p.page_size - 1) >> p.page_shift;
+        int page = j < have ? p.block_table[(size_t)b * p.max_pages + j] : fresh_page(asked, j - have);
+        if (page < 0 || page >= p.n_pages) {
+          if (j < have) record_error(p.status, kErrInvalid, 302);
+        } else {
+          slot = (page << p.page_shift) + (pos & (p.page_size - 1));
+        }
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+}
+
+cudaError_t launch_page_map(const PageMapParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const int smem_max = 2 * kPagedMaxSeqs * (int)sizeof(int);
+  const cudaError_t e = ensure_dynamic_smem(page_map_kernel, smem_max, done);
+  if (e != cudaSuccess) return e;
+  const int blocks = std::min((p.max_tokens + kMapTokensPerBlock - 1) / kMapTokensPerBlock, 148 * 2);
+  return launch_dependent(page_map_kernel, dim3(std::max(blocks, 1)), dim3(kMapThreads), 2 * p.B * sizeof(int), st, p);
+}
+
+// ============================================================= paged append
+// The prefill prologue's arithmetic (norm x / sqrt(mean(x^2) + 1e-6) * gamma in
+// fp32, angles in double, rotation in fp32, one rounding to bf16), one warp on a
+// share of one token's rows; the keys go to their slots.  HBM-bound on prompts:
+// (Hq + 2 Hkv) * D * 2 bytes read and as many written per token.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 2;
+
+__device__ __forceinline__ void unpack8(const uint4 u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAppendParams p) {
+  constexpr int H2 = D / 2;
+  constexpr int LPR = D / 16;    // lanes per row: each holds 8 features of each half
+  constexpr int RPW = 32 / LPR;  // rows per warp step
+  constexpr int FPL = (H2 + 31) / 32;
+  __shared__ __align__(16) float gam[2 * D];  // q gain, then k gain
+  __shared__ double inv_freq_s[H2];
+  const int lane = threadIdx.x & 31;
+  const int li = lane % LPR, sub = lane / LPR;
+  const int d1 = li * 8;
+  const int heads = p.Hq + p.Hkv;  // Hq = 0 without queries
+  for (int i = threadIdx.x; i < H2; i += kAppendThreads) inv_freq_s[i] = p.inv_freq[i];
+  griddep_wait();
+  griddep_launch();
+  for (int i = threadIdx.x; i < 2 * D; i += kAppendThreads)
+    gam[i] = i >= D ? p.k_gamma[i - D] : p.Hq > 0 ? p.q_gamma[i] : 0.f;
+  __syncthreads();
+
+  // `share` of a token's rows: warps_per_token warps split them.
+  const long long items = (long long)p.T * p.warps_per_token;
+  const long long stride = (long long)gridDim.x * (kAppendThreads / 32);
+  for (long long it = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); it < items; it += stride) {
+    const int t = (int)(it / p.warps_per_token), share = (int)(it % p.warps_per_token);
+    const int slot = p.slots[t];
+    const bool keep = slot >= 0 && slot < p.n_slots;
+    if (slot >= p.n_slots && lane == 0 && share == 0) record_error(p.status, kErrInvalid, 310);
+    float cl[FPL], sl[FPL];
+    const double pos = (double)p.positions[t] / p.interp;
+#pragma unroll
+    for (int i = 0; i < FPL; ++i) {
+      const int f = FPL * lane + i;
+      cl[i] = 1.f;
+      sl[i] = 0.f;
+      if (f < H2) {
+        double sd, cd;
+        sincos(pos * inv_freq_s[f], &sd, &cd);
+        cl[i] = (float)cd;
+        sl[i] = (float)sd;
+      }
+    }
+    float c[8], s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = __shfl_sync(0xffffffffu, cl[e % FPL], (d1 + e) / FPL);
+      s[e] = __shfl_sync(0xffffffffu, sl[e % FPL], (d1 + e) / FPL);
+    }
+    // First row of the slot: rows of one (page, head) are P apart from the next head's.
+    const size_t page = keep ? (size_t)(slot >> p.page_shift) : 0;
+    const size_t crow0 = ((page * p.Hkv) << p.page_shift) + (keep ? slot & ((1 << p.page_shift) - 1) : 0);
+    const __nv_bfloat16* qrow = p.q + (size_t)t * p.Hq * D;
+    const __nv_bfloat16* krow = p.k + (size_t)t * p.Hkv * D;
+    for (int h0 = share * RPW * kAppendUnroll; h0 < heads; h0 += p.warps_per_token * RPW * kAppendUnroll) {
+      uint4 xa[kAppendUnroll], xb[kAppendUnroll];
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int h = h0 + u * RPW + sub;
+        xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < heads && (h < p.Hq || keep)) {
+          const __nv_bfloat16* src = h < p.Hq ? qrow + h * D : krow + (h - p.Hq) * D;
+          xa[u] = __ldg(reinterpret_cast<const uint4*>(src + d1));
+          xb[u] = __ldg(reinterpret_cast<const uint4*>(src + H2 + d1));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        float x[16];
+        unpack8(xa[u], x);
+        unpack8(xb[u], x + 8);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const int h = h0 + u * RPW + sub;
+        if (h >= heads || (h >= p.Hq && !keep)) continue;
+        const bool is_q = h < p.Hq;
+        const float rinv = rsqrtf(ss * (1.0f / D) + 1e-6f);
+        const float* gs = gam + (is_q ? 0 : D);
+        float g[16];
+        *reinterpret_cast<float4*>(g) = *reinterpret_cast<const float4*>(gs + d1);
+        *reinterpret_cast<float4*>(g + 4) = *reinterpret_cast<const float4*>(gs + d1 + 4);
+        *reinterpret_cast<float4*>(g + 8) = *reinterpret_cast<const float4*>(gs + H2 + d1);
+        *reinterpret_cast<float4*>(g + 12) = *reinterpret_cast<const float4*>(gs + H2 + d1 + 4);
+        float o[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y1 = x[e] * rinv * g[e];
+          const float y2 = x[8 + e] * rinv * g[8 + e];
+          o[e] = y1 * c[e] - y2 * s[e];
+          o[8 + e] = y1 * s[e] + y2 * c[e];
+        }
+        if (is_q) {
+          __nv_bfloat16* dst = p.q_hat + ((size_t)t * p.Hq + h) * D;
+          *reinterpret_cast<uint4*>(dst + d1) = pack8(o);
+          *reinterpret_cast<uint4*>(dst + H2 + d1) = pack8(o + 8);
+        } else {
+          const int kh = h - p.Hq;
+          const size_t at = (crow0 + ((size_t)kh << p.page_shift)) * D;
+          *reinterpret_cast<uint4*>(p.k_pages + at + d1) = pack8(o);
+          *reinterpret_cast<uint4*>(p.k_pages + at + H2 + d1) = pack8(o + 8);
+          const __nv_bfloat16* vsrc = p.v + ((size_t)t * p.Hkv + kh) * D;
+          *reinterpret_cast<uint4*>(p.v_pages + at + d1) = __ldg(reinterpret_cast<const uint4*>(vsrc + d1));
+          *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = __ldg(reinterpret_cast<const uint4*>(vsrc + H2 + d1));
+        }
+      }
+    }
+  }
+}
+
+cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st) {
+  // A few tokens: split each one's rows over more warps, up to one step of rows each.
+  const int rows_step = 32 / (D / 16) * kAppendUnroll, heads = p.Hq + p.Hkv;
+  p.warps_per_token = 1;
+  while (p.warps_per_token < 8 && p.warps_per_token * rows_step < heads && (long long)p.T * p.warps_per_token < 148 * 16)
+    p.warps_per_token *= 2;
+  const long long items = (long long)p.T * p.warps_per_token;
+  const unsigned blocks = (unsigned)std::min<long long>((items + kAppendThreads / 32 - 1) / (kAppendThreads / 32), 148 * 8);
+  switch (D) {
+    case 64: return launch_dependent(paged_append_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
+    case 128: return launch_dependent(paged_append_kernel<128>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
+    case 256: return launch_dependent(paged_append_kernel<256>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// ============================================================== page bounds
+// HBM-bound: one warp reads the rows of one (page, kv head) once, keeping the
+// largest and smallest value of 8 features per lane in packed bf16.
+constexpr int kBoundsThreads = 256;
+constexpr int kBoundsUnroll = 8;  // 16-byte loads in flight per lane
+
+// The largest e with amax * 2^e <= 127, kept within -50 .. 50 (so that products
+// of two scaled sums stay finite in fp32), from the bits of a bf16 amax >= 0:
+// amax = 2^x (1 + M / 128) gives e = 6 - x, one less when 64 + M / 2 > 127.
+__device__ __forceinline__ int bound_exponent(uint32_t bf16_bits) {
+  const int x = (int)((bf16_bits >> 7) & 0xff) - 127, m = bf16_bits & 0x7f;
+  return max(-50, min(50, 6 - x - (m == 127 ? 1 : 0)));
+}
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
+
+template <int D>
+__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsParams p) {
+  extern __shared__ int bounds_smem[];  // [B + 1] touched pages before each sequence
+  __shared__ int warp_sums[kBoundsThreads / 32];
+  constexpr int LPT = D / 8;     // lanes per row
+  constexpr int TPS = 32 / LPT;  // rows per warp-wide load
+  griddep_wait();
+  griddep_launch();
+  const long long room = (long long)p.max_pages << p.page_shift;
+  block_prefix(p.B, bounds_smem, warp_sums, [&](int b) {
+    const int L = p.seq_lens[b], old = p.old_lens[b];
+    if (L < 0 || L > room || old < 0) {
+      if (blockIdx.x == 0) record_error(p.status, kErrInvalid, 320);
+      return 0;
+    }
+    return max(0, ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift));
+  });
+  const long long units = (long long)bounds_smem[p.B] * p.Hkv;
+  const int lane = threadIdx.x & 31, li = lane % LPT, sub = lane / LPT;
+  const int P = 1 << p.page_shift;
+  for (long long u = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += (long long)gridDim.x * (kBoundsThreads / 32)) {
+    const int pj = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
+    const int b = find_row(bounds_smem, p.B, pj, 1);
+    const int j = (p.old_lens[b] >> p.page_shift) + pj - bounds_smem[b];
+    const int rows = min(P, p.seq_lens[b] - (j << p.page_shift));
+    const int page = p.block_table[(size_t)b * p.max_pages + j];
+    if (page < 0 || page >= p.n_pages) {
+      if (lane == 0) record_error(p.status, kErrInvalid, 321);
+      continue;
+    }
+    if (rows <= 0) continue;  // the old length at a page's end
+    const uint4* base = reinterpret_cast<const uint4*>(p.k_pages + ((((size_t)page * p.Hkv + h) << p.page_shift)) * D) + li;
+    const __nv_bfloat162 ninf = __floats2bfloat162_rn(-INFINITY, -INFINITY), pinf = __floats2bfloat162_rn(INFINITY, INFINITY);
+    __nv_bfloat162 mx[4], mn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mx[i] = ninf;
+      mn[i] = pinf;
+    }
+    for (int r0 = 0; r0 < rows; r0 += TPS * kBoundsUnroll) {
+      uint4 x[kBoundsUnroll];
+#pragma unroll
+      for (int k = 0; k < kBoundsUnroll; ++k) {
+        const int r = min(r0 + k * TPS + sub, rows - 1);  // a row read twice changes nothing
+        x[k] = __ldg(base + (size_t)r * LPT);
+      }
+#pragma unroll
+      for (int k = 0; k < kBoundsUnroll; ++k) {
+        const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&x[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the _nan forms keep a NaN
+          mx[i] = __hmax2_nan(mx[i], v[i]);
+          mn[i] = __hmin2_nan(mn[i], v[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int off = LPT; off < 32; off <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mx[i] = __hmax2_nan(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+        mn[i] = __hmin2_nan(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
+      }
+    }
+    // Bits of |x| of bf16 values order as integers; a NaN's are above infinity's.
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = *reinterpret_cast<uint32_t*>(&mx[i]) & 0x7fff7fffu, c = *reinterpret_cast<uint32_t*>(&mn[i]) & 0x7fff7fffu;
+      amax = max(amax, max(max(a & 0xffffu, a >> 16), max(c & 0xffffu, c >> 16)));
+    }
+#pragma unroll
+    for (int off = LPT / 2; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const int e = bound_exponent(amax);
+    const float unit = exp2_int(e);
+    uint32_t hi8[2] = {0, 0}, lo8[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 a = mx[i / 2], c = mn[i / 2];
+      const float fa = __bfloat162float(i % 2 ? a.y : a.x), fc = __bfloat162float(i % 2 ? c.y : c.x);
+      // Outward: the largest up, the smallest down (a product that underflows still counts as nonzero).
+      float ua = ceilf(fa * unit), uc = floorf(fc * unit);
+      if (fa > 0.f) ua = fmaxf(ua, 1.f);
+      if (fc < 0.f) uc = fminf(uc, -1.f);
+      ua = fa != fa ? 127.f : fminf(fmaxf(ua, -127.f), 127.f);
+      uc = fc != fc ? -127.f : fminf(fmaxf(uc, -127.f), 127.f);
+      hi8[i / 4] |= ((uint32_t)(int)ua & 0xffu) << (8 * (i % 4));
+      lo8[i / 4] |= ((uint32_t)(int)uc & 0xffu) << (8 * (i % 4));
+    }
+    if (sub == 0) {
+      const size_t ph = (size_t)page * p.Hkv + h;
+      uint2* dst = reinterpret_cast<uint2*>(p.bounds + ph * 2 * D);
+      dst[li] = make_uint2(hi8[0], hi8[1]);
+      dst[LPT + li] = make_uint2(lo8[0], lo8[1]);
+      if (li == 0) p.exps[ph] = (int8_t)e;
+    }
+  }
+}
+
+cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st) {
+  const long long most = ((long long)p.B * p.max_pages * p.Hkv + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
+  const dim3 grid((unsigned)std::min<long long>(most, 148 * 4)), block(kBoundsThreads);
+  const size_t smem = (p.B + 1) * sizeof(int);
+  switch (D) {
+    case 64: return launch_dependent(page_bounds_kernel<64>, grid, block, smem, st, p);
+    case 128: return launch_dependent(page_bounds_kernel<128>, grid, block, smem, st, p);
+    case 256: return launch_dependent(page_bounds_kernel<256>, grid, block, smem, st, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// ============================================================== page scores
+// score(b, kv head, page) = max over the group's query heads of
+//     2^-(eq + ek) * sum_d (q8_d >= 0 ? q8_d * max8_d : q8_d * min8_d),
+// with q8 = the query's features rounded to 8 bits with a power-of-two exponent
+// eq of its own.  As a product: [q8+, q8-] (2D features) with [max8, min8], whole
+// numbers below 2^24 in any order, so the scores are exact and the selection does
+// not depend on how they are summed.  HBM-bound: 2D + 1 bytes per (page, kv head).
+//
+// One warp takes 64 pages of one (sequence, kv head), 16 at a time, as
+// mma.m16n8k32 of 8-bit whole numbers: rows are pages, columns the group's heads.
+// Each lane loads 16-byte pieces of two pages' bounds straight into its A
+// fragments; the order of the features inside a product is free, so the pieces
+// are used as they come and the query is laid out to match.
+constexpr int kScoreThreads = 256;
+constexpr int kScorePages = 64;  // pages of one warp task
+
+__device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(PageSelectParams p) {
+  constexpr int WARPS = kScoreThreads / 32;
+  constexpr int PIECES = 2 * D / 64;  // 16-byte pieces of a page's bounds per lane
+  constexpr int FPL = D / 32;         // query features per lane
+  extern __shared__ int score_smem[];  // [B + 1] tasks before each sequence
+  __shared__ int warp_sums[WARPS];
+  __shared__ __align__(16) int8_t q8[WARPS][8][2 * D];
+  __shared__ float q_unit[WARPS][8];
+  griddep_wait();
+  griddep_launch();
+  const long long room = (long long)p.max_pages << p.page_shift;
+  block_prefix(p.B, score_smem, warp_sums, [&](int b) {
+    const int L = p.seq_lens[b];
+    if (L < 0 || L > room) {
+      if (blockIdx.x == 0) record_error(p.status, kErrInvalid, 330);
+      return 0;
+    }
+    const int np = (L + (1 << p.page_shift) - 1) >> p.page_shift;
+    return np <= p.n_select ? 0 : (np + kScorePages - 1) / kScorePages;  // no choice, no scores
+  });
+  const long long tasks = (long long)score_smem[p.B] * p.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = lane >> 2, c = lane & 3;
+  for (long long u = (long long)blockIdx.x * WARPS + warp; u < tasks; u += (long long)gridDim.x * WARPS) {
+    const int tj = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
+    const int b = find_row(score_smem, p.B, tj, 1);
+    const int page0 = (tj - score_smem[b]) * kScorePages;
+    const int np = (p.seq_lens[b] + (1 << p.page_shift) - 1) >> p.page_shift;
+    // Physical pages of the task's 64 (the pages past the last one repeat it).
+    int ids[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = min(page0 + 32 * i + lane, np - 1);
+      int id = p.block_table[(size_t)b * p.max_pages + j];
+      if (id < 0 || id >= p.n_pages) {
+        record_error(p.status, kErrInvalid, 331);
+        id = -1;
+      }
+      ids[i] = id;
+    }
+    // The group's queries in 8 bits: positive parts, then negative parts.
+    __syncwarp();
+    for (int g = 0; g < 8; ++g) {
+      float x[FPL];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int i = 0; i < FPL; ++i) {
+        x[i] = g < p.G ? __bfloat162float(p.q_hat[((size_t)b * p.Hq + h * p.G + g) * D + i * 32 + lane]) : 0.f;
+        if (x[i] != x[i]) x[i] = 0.f;
+        amax = max(amax, (__float_as_uint(x[i]) & 0x7fffffffu) >> 16);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      const int e = bound_exponent(amax);
+      const float unit = exp2_int(e);
+#pragma unroll
+      for (int i = 0; i < FPL; ++i) {
+        const int v = (int)fminf(fmaxf(rintf(x[i] * unit), -127.f), 127.f);
+        q8[warp][g][i * 32 + lane] = (int8_t)max(v, 0);
+        q8[warp][g][D + i * 32 + lane] = (int8_t)min(v, 0);
+      }
+      if (lane == 0) q_unit[warp][g] = exp2_int(-e);
+    }
+    __syncwarp();
+    uint4 bq[PIECES];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) bq[k] = *reinterpret_cast<const uint4*>(&q8[warp][row][c * 16 + 64 * k]);
+    const float unit0 = q_unit[warp][2 * c], unit1 = q_unit[warp][2 * c + 1];
+    float* dst = p.scores + ((size_t)b * p.Hkv + h) * p.max_pages;
+#pragma unroll
+    for (int grp = 0; grp < kScorePages / 16; ++grp) {
+      const int j0 = page0 + grp * 16;
+      if (j0 >= np) break;
+      const int id0 = __shfl_sync(0xffffffffu, ids[grp / 2], (grp % 2) * 16 + row);
+      const int id1 = __shfl_sync(0xffffffffu, ids[grp / 2], (grp % 2) * 16 + row + 8);
+      const size_t ph0 = (size_t)max(id0, 0) * p.Hkv + h, ph1 = (size_t)max(id1, 0) * p.Hkv + h;
+      const uint4* s0 = reinterpret_cast<const uint4*>(p.bounds + ph0 * 2 * D) + c;
+      const uint4* s1 = reinterpret_cast<const uint4*>(p.bounds + ph1 * 2 * D) + c;
+      uint4 a0[PIECES], a1[PIECES];
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        a0[k] = __ldg(s0 + 4 * k);
+        a1[k] = __ldg(s1 + 4 * k);
+      }
+      const int e0 = p.exps[ph0], e1 = p.exps[ph1];
+      int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, bq[k].x, bq[k].y);
+        mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, bq[k].z, bq[k].w);
+      }
+      // acc: page row / row + 8, heads 2c and 2c + 1.
+      const float x0 = 2 * c < p.G ? (float)acc[0] * unit0 : -INFINITY, x1 = 2 * c + 1 < p.G ? (float)acc[1] * unit1 : -INFINITY;
+      const float y0 = 2 * c < p.G ? (float)acc[2] * unit0 : -INFINITY, y1 = 2 * c + 1 < p.G ? (float)acc[3] * unit1 : -INFINITY;
+      float s_lo = fmaxf(x0, x1) * exp2_int(-e0), s_hi = fmaxf(y0, y1) * exp2_int(-e1);
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        s_lo = fmaxf(s_lo, __shfl_xor_sync(0xffffffffu, s_lo, off));
+        s_hi = fmaxf(s_hi, __shfl_xor_sync(0xffffffffu, s_hi, off));
+      }
+      if (c == 0) {  // a page with no valid id is chosen last
+        if (j0 + row < np) dst[j0 + row] = id0 < 0 ? -INFINITY : s_lo;
+        if (j0 + row + 8 < np) dst[j0 + row + 8] = id1 < 0 ? -INFINITY : s_hi;
+      }
+    }
+  }
+}
+
+// ================================================================ page pick
+// The newest page and the n_select - 1 highest scores of the others, equal
+// scores by the lower page, in ascending order.  One block per (sequence, kv
+// head): the scores as ordered integers, the threshold by four 8-bit digits,
+// then an ordered write.
+constexpr int kPickThreads = 256;
+
+// Ascending order of the floats (no NaN) as ascending unsigned integers; -0 counts as +0.
+__device__ __forceinline__ uint32_t ordered_bits(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParams p) {
+  constexpr int WARPS = kPickThreads / 32;
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t s_prefix, s_left;
+  __shared__ int s_gt[WARPS], s_eq[WARPS];
+  griddep_wait();
+  griddep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int L = p.seq_lens[b];
+  const long long room = (long long)p.max_pages << p.page_shift;
+  const int np = L < 0 || L > room ? 0 : (L + (1 << p.page_shift) - 1) >> p.page_shift;
+  int32_t* out = p.pages + ((size_t)b * p.Hkv + h) * p.n_select;
+  if (np <= p.n_select) {
+    for (int i = tid; i < p.n_select; i += kPickThreads) out[i] = i < np ? i : -1;
+    return;
+  }
+  const int k = p.n_select - 1, n = np - 1;  // k of the n pages before the newest
+  if (tid == 0) out[k] = n;
+  if (k == 0) return;
+  const float* sc = p.scores + ((size_t)b * p.Hkv + h) * p.max_pages;
+  uint32_t prefix = 0, left = k;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    hist[tid] = 0;
+    __syncthreads();
+    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+    for (int i = tid; i < n; i += kPickThreads) {
+      const uint32_t u = ordered_bits(sc[i]);
+      if ((u & above) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // Lane l holds digits 255 - 8l .. 248 - 8l: the digit at which the count from above reaches `left`.
+      uint32_t d[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = hist[255 - (lane * 8 + i)];
+        sum += d[i];
+      }
+      uint32_t inc = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+      }
+      uint32_t before = inc - sum;
+      if (before < left && inc >= left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < left && before + d[i] >= left) {
+            s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
+            s_left = left - before;
+            before = left;  // found
+          } else {
+            before += d[i];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
+  }
+  // `prefix` is the k-th highest score; `left` of the pages that have it are taken.
+  const int per = ((n + WARPS - 1) / WARPS + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
+  int gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t u = ordered_bits(sc[i]);
+    gt += u > prefix;
+    eq += u == prefix;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, off);
+    eq += __shfl_xor_sync(0xffffffffu, eq, off);
+  }
+  if (lane == 0) {
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
+  }
+  __syncthreads();
+  int gt0 = 0, eq0 = 0;
+  for (int w = 0; w < warp; ++w) {
+    gt0 += s_gt[w];
+    eq0 += s_eq[w];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t u = i + lane < i1 ? ordered_bits(sc[i + lane]) : 0u;
+    const bool is_gt = i + lane < i1 && u > prefix, is_eq = i + lane < i1 && u == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    const int eq_rank = eq0 + __popc(be & below);
+    const int at = gt0 + __popc(bg & below) + min(eq_rank, (int)left);
+    if (is_gt || (is_eq && eq_rank < (int)left)) out[at] = i + lane;
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
+  }
+}
+
+cudaError_t launch_page_scores(const PageSelectParams& p, int D, cudaStream_t st) {
+  const long long most = ((long long)p.B * ((p.max_pages + kScorePages - 1) / kScorePages) * p.Hkv + 7) / 8;
+  const dim3 grid((unsigned)std::min<long long>(most, 148 * 4)), block(kScoreThreads);
+  const size_t smem = (p.B + 1) * sizeof(int);
+  switch (D) {
+    case 64: return launch_dependent(page_scores_kernel<64>, grid, block, smem, st, p);
+    case 128: return launch_dependent(page_scores_kernel<128>, grid, block, smem, st, p);
+    case 256: return launch_dependent(page_scores_kernel<256>, grid, block, smem, st, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_page_pick(const PageSelectParams& p, cudaStream_t st) {
+  return launch_dependent(page_pick_kernel, dim3(p.Hkv, p.B), dim3(kPickThreads), 0, st, p);
+}
+
+}  // namespace g3

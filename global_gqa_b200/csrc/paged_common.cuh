@@ -1,0 +1,63 @@
+// What the paged-cache kernels share.
+//
+// A paged cache of one layer is k_pages, v_pages [n_pages, Hkv, P, D] bf16: one
+// (page, kv head) is P consecutive rows.  Logical page j of sequence b is
+// block_table[b, j]; its token t sits in row t % P of logical page t / P.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "g3_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace g3 {
+
+// Lets the next kernel in the stream, when it was launched as a programmatic
+// dependent, take its place on the SMs early; it still waits for this one's end.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Inclusive prefix sums of count(b), b < n, into pref[1 .. n], pref[0] = 0, by
+// the whole block (a multiple of 32 threads; `warp_sums` holds one int per
+// warp).  Every block of a grid repeats it: a few microseconds at the largest n,
+// for one launch less and no order between blocks.
+template <class F>
+__device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F&& count) {
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + threads - 1) / threads;  // consecutive entries of each thread
+  const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    sum += count(i);
+    pref[i + 1] = sum;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int before = inc - sum;
+  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  for (int i = i0; i < i1; ++i) pref[i + 1] += before;
+  if (tid == 0) pref[0] = 0;
+  __syncthreads();
+}
+
+// The b with pref[b] * scale <= x < pref[b + 1] * scale; 0 <= x < pref[n] * scale.
+__device__ __forceinline__ int find_row(const int* pref, int n, long long x, int scale) {
+  int lo = 0, hi = n;  // pref[lo] * scale <= x < pref[hi] * scale
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)pref[mid] * scale <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace g3

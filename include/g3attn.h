@@ -288,6 +288,160 @@ g3_status g3attn_decode_no_alloc(const void* q, const void* k_new, const void* v
                                  int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                  void* out, void* stream);
 
+/* -------------------------------------------------------------- paged cache
+ * The decode cache in pages: instead of one [capacity, D] stretch per sequence
+ * and kv head, a layer has a pool of pages that sequences take as they grow.
+ *
+ *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, D]: rotated keys, values.
+ *              page_size in {16, 32, 64, 128, 256}; n_pages * page_size < 2^31
+ *   block_table int32 [B, max_pages]: physical page of each logical page of a
+ *              sequence; token t is row t % page_size of logical page
+ *              t / page_size.  Entries that a call has no need of may hold
+ *              anything (a local layer: pages wholly before the window)
+ *   slot       physical page * page_size + row, as one number
+ *   status     optional int32 [2] on the device, zero before its first use.
+ *              The first error that a paged call meets in device-resident
+ *              values is recorded there and stays until
+ *              g3attn_check_device_error(status, stream) reports and clears
+ *              it; any number of calls may share it.  NULL: not recorded.
+ *   At most 8192 sequences, and 8 query heads per kv head, in one call.
+ * The calls are ordered by their stream alone and may be captured in a graph.
+ * A serving step is: page_map once for all layers, then per layer paged_append,
+ * (page_bounds and page_select on a sparse global layer,) paged_decode.
+ */
+
+/*
+ * Block tables, slots and positions of one step's new tokens.
+ *
+ *   old_lens, new_lens int32 [B]  tokens cached before this step and added by
+ *              it (0: none, the sequence waits)
+ *   block_table in place: entries ceil(old / page_size) ..
+ *              ceil((old + new) / page_size) - 1 of each sequence are written
+ *   free_pages int32 [free_capacity], a ring of free page numbers, with
+ *   free_state int32 [2] = {head, count}: pages are taken from the head on, in
+ *              the order of the sequences.  To give pages back, write them
+ *              behind the last one ((head + count) % free_capacity) and raise count
+ *   max_tokens rows of slots and positions
+ *   seq_lens   int32 [B]  old + new, or old where the sequence was refused
+ *   cu_tokens  int32 [B + 1]  first row of each sequence's new tokens in the
+ *              packed order of the sequences (refused ones keep their rows)
+ *   slots, positions int32 [max_tokens]  of each packed row; -1 and 0 for
+ *              refused sequences and behind the last row
+ *   free_state_out int32 [2]
+ * A sequence is refused, and recorded in status, when a length is negative,
+ * old + new exceeds max_pages * page_size, its rows exceed max_tokens, or its
+ * pages and those of the sequences before it exceed the ring's count (a
+ * sequence that needs no new page is served all the same).  A free page number
+ * outside 0 .. n_pages-1 becomes table entry -1 with slots -1, and a known page
+ * that is out of range gives slots -1, both recorded.  No output may overlap an
+ * input or another output (G3_ERR_INVALID_ARG).
+ */
+g3_status g3attn_page_map(const int32_t* old_lens, const int32_t* new_lens, int32_t B,
+                          int32_t* block_table, int32_t max_pages,
+                          const int32_t* free_pages, int32_t free_capacity, const int32_t* free_state,
+                          int32_t page_size, int32_t n_pages, int32_t max_tokens,
+                          int32_t* seq_lens, int32_t* cu_tokens, int32_t* slots, int32_t* positions,
+                          int32_t* free_state_out, int32_t* status, void* stream);
+
+/*
+ * New tokens into the pages: QK-norm and RoPE of packed tokens (steps 1 and 2
+ * above), a prompt's or one per sequence.
+ *
+ *   q          bf16 [T, Hq, D] raw queries with q_gamma fp32 [D] and q_hat
+ *              bf16 [T, Hq, D] (output: normalised and rotated), or all three
+ *              NULL with Hq = 0
+ *   k, v       bf16 [T, Hkv, D] raw keys, values;  k_gamma fp32 [D]
+ *   positions  int32 [T]  RoPE positions
+ *   slots      int32 [T]  where each token's rotated key and value go; below 0:
+ *              nowhere (its q_hat row is still written).  Slots of one call are
+ *              distinct (of equal ones, rows of either token may remain); a
+ *              slot past the last page is recorded and the token not cached
+ *   T          >= 0 (0: nothing is enqueued)
+ */
+g3_status g3attn_paged_append(const void* q, const void* k, const void* v,
+                              const float* q_gamma, const float* k_gamma,
+                              const int32_t* positions, const int32_t* slots,
+                              void* k_pages, void* v_pages, int32_t n_pages, int32_t page_size,
+                              float rope_base, float interp_factor,
+                              int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                              void* q_hat, int32_t* status, void* stream);
+
+/*
+ * Bounds of the cached keys of each page, for page_select: the feature-wise
+ * largest and smallest key over the page's filled rows, rounded outward to 8
+ * bits with one power-of-two exponent per (page, kv head).
+ *
+ *   old_lens, seq_lens int32 [B]  the pages that hold tokens old .. seq_len-1
+ *              are renewed from all their rows below seq_len (a page that is
+ *              filled up by one step is renewed as a whole)
+ *   bounds     int8 [n_pages, Hkv, 2, D]: min(127, ceil(largest * 2^e)), then
+ *              max(-127, floor(smallest * 2^e))
+ *   exps       int8 [n_pages, Hkv]: e, the largest with max|key| * 2^e <= 127,
+ *              within -50 .. 50
+ * A NaN counts as unbounded both ways.  Bad lengths or page numbers are
+ * recorded in status and skipped.
+ */
+g3_status g3attn_page_bounds(const void* k_pages, const int32_t* block_table,
+                             const int32_t* old_lens, const int32_t* seq_lens,
+                             int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                             int32_t Hkv, int32_t D, int8_t* bounds, int8_t* exps,
+                             int32_t* status, void* stream);
+
+/* Bytes of workspace g3attn_page_select needs (0 if the sizes are invalid); 256-byte aligned. */
+size_t g3attn_page_select_workspace_size(int32_t B, int32_t Hkv, int32_t max_pages);
+
+/*
+ * The pages that each query is to attend to: for every sequence and kv head the
+ * page of the newest token and the n_select - 1 others with the highest score,
+ *   score = max over the group's query heads of
+ *           sum_d (q8_d >= 0 ? q8_d * bounds[0][d] : q8_d * bounds[1][d]) * 2^-(eq + exps)
+ * with q8 = q_hat rounded to the nearest 8-bit number under a power-of-two
+ * exponent eq as in page_bounds: an upper bound of q . k over the page up to the
+ * rounding of q.  Equal scores: the lower page.  Whole-number sums, so the
+ * result does not depend on their order.
+ *
+ *   q_hat      bf16 [B, Hq, D] from paged_append (a NaN feature counts as 0)
+ *   seq_lens   int32 [B] tokens cached, the new one included
+ *   pages      int32 [B, Hkv, n_select]  logical pages, ascending; -1 behind the
+ *              last one where a sequence has fewer
+ *   workspace  >= g3attn_page_select_workspace_size(B, Hkv, max_pages) bytes
+ */
+g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8_t* exps,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                             int32_t Hq, int32_t Hkv, int32_t D, int32_t n_select, int32_t* pages,
+                             void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace g3attn_paged_decode needs (0 if the sizes are invalid); 256-byte aligned. */
+size_t g3attn_paged_decode_workspace_size(int32_t B, int32_t D);
+
+/*
+ * Attention of one new token per sequence over its pages (steps 3 and 4 above).
+ *
+ *   q_hat      bf16 [B, Hq, D] from paged_append
+ *   seq_lens   int32 [B] tokens cached, the new one included: a GLOBAL layer
+ *              sees all of them, a LOCAL one the last `window`.  0: the sequence
+ *              is idle
+ *   pages      optional int32 [B, Hkv, n_select], GLOBAL layers: attend to these
+ *              logical pages only, as page_select gives them (ascending; -1
+ *              pads the end).  NULL with n_select = 0: to all
+ *   out        bf16 [B, Hq, D];  lse optional fp32 [B, Hq] (natural log, as prefill's)
+ *   workspace  >= g3attn_paged_decode_workspace_size(B, D) bytes
+ * A sequence that sees nothing (idle, or a length out of range, which is
+ * recorded) gets a zero row and an lse of -infinity.  A page number out of
+ * range, or a list entry that is out of range or not above the one before it,
+ * is recorded and left out.  Rows of a page that hold no visible token do not
+ * matter, NaN included.
+ */
+g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* seq_lens,
+                              const int32_t* pages, int32_t n_select,
+                              g3_layer_kind layer_kind, int32_t window,
+                              int32_t B, int32_t max_pages, int32_t n_pages, int32_t page_size,
+                              int32_t Hq, int32_t Hkv, int32_t D,
+                              void* out, float* lse,
+                              void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* ----------------------------------------------------------------- checking
  * Synchronises `stream`, then returns (and clears) the first device-side error
  * recorded in `workspace` by the last prefill/decode call that used it:
