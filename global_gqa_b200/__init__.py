@@ -460,9 +460,24 @@ def soft_tokens(patches, gamma, grid_h: int, grid_w: int, pool: int = 4, *, out=
 
 # ------------------------------------------------------------- paged cache
 # A decode step makes several of these calls per layer, each a few microseconds
-# on the GPU: arguments that are right pass one short test each, the messages
-# come from the checks above only when one is not.
+# on the GPU.  Where a call is plain (outputs made here, the current stream and
+# device) the module _paged checks its arguments, allocates and calls the library;
+# it answers None when something is not as expected, and the ordinary way below
+# follows, which words the error or serves the options.
 _paged_statuses = {}
+_quick = None
+
+
+def _load_quick():
+    global _quick
+    if _quick is None:
+        lib()
+        _torch()
+        if not os.path.exists(os.path.join(HERE, "_paged.so")):
+            raise RuntimeError("_paged.so is missing: build it with `python -m global_gqa_b200.build`")
+        from . import _paged
+        _quick = _paged
+    return _quick
 
 
 def paged_status(device=None):
@@ -483,6 +498,7 @@ def paged_status(device=None):
             st = torch.zeros(2, dtype=torch.int32, device=dev)
             torch.cuda.current_stream(dev).synchronize()  # any stream may use it from now on
         st = _paged_statuses.setdefault(dev.index, st)
+        _load_quick().set_status(dev.index, st)
     return st
 
 
@@ -498,12 +514,22 @@ def _arg(t, name, dtype, shape, device) -> int:
     raise ValueError(f"{name} is not usable")
 
 
-def _dims(t, name, dtype, n: int):
-    """The shape of a leading argument, checked on its own."""
-    _req(t, name, dtype)
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
-    return t.shape
+def _shape(t, name, n: int):
+    """The shape of an argument that the others' shapes follow from (its type and place are left to _arg)."""
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {tuple(shape)}")
+    return shape
+
+
+def _gpu_of(t, name):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device (no CPU path exists)")
+    return dev
 
 
 def _paged_call(fn, device, stream, status, *args) -> None:
@@ -514,16 +540,17 @@ def _paged_call(fn, device, stream, status, *args) -> None:
         if status is None:
             status = paged_status(device)
     st = _arg(status, "status", torch.int32, (2,), device)
+    sp = _stream_ptr(stream, device)
     if torch.cuda.current_device() == device.index:
-        code = getattr(lib(), fn)(*args, st, _stream_ptr(stream, device))
+        code = getattr(_lib or lib(), fn)(*args, st, sp)
     else:
         with torch.cuda.device(device):
-            code = getattr(lib(), fn)(*args, st, _stream_ptr(stream, device))
+            code = getattr(_lib or lib(), fn)(*args, st, sp)
     if code != 0:
         _check(code, fn)
 
 
-def _empty(stream, device, shape, dtype):
+def _empty(stream, device, dtype, *shape):
     """An output or workspace whose memory belongs to the stream that the call runs on."""
     torch = _torch()
     if stream is None:
@@ -551,18 +578,23 @@ def page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size:
     cu_tokens [B+1], slots [max_tokens], positions [max_tokens], free_state [2]),
     all int32; `out` may hold preallocated ones under the same keys.
     """
-    torch = _torch()
-    i32 = torch.int32
-    B, = _dims(old_lens, "old_lens", i32, 1)
-    _, max_pages = _dims(block_table, "block_table", i32, 2)
-    dev = old_lens.device
-    cap, = _dims(free_pages, "free_pages", i32, 1)
+    if out is None and stream is None:
+        r = (_quick or _load_quick()).page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size, n_pages,
+                                               max_tokens, status)
+        if r is not None:
+            return r
+    i32 = _torch().int32
+    B, = _shape(old_lens, "old_lens", 1)
+    max_pages = _shape(block_table, "block_table", 2)[1]
+    cap, = _shape(free_pages, "free_pages", 1)
+    dev = _gpu_of(old_lens, "old_lens")
     r = dict(out) if out is not None else {}
     for name, n in (("seq_lens", B), ("cu_tokens", B + 1), ("slots", max_tokens), ("positions", max_tokens),
                     ("free_state", 2)):
         if name not in r:
-            r[name] = _empty(stream, dev, (n,), i32)
-    _paged_call("g3attn_page_map", dev, stream, status, old_lens.data_ptr(), _arg(new_lens, "new_lens", i32, (B,), dev), B,
+            r[name] = _empty(stream, dev, i32, n)
+    _paged_call("g3attn_page_map", dev, stream, status, _arg(old_lens, "old_lens", i32, (B,), dev),
+                _arg(new_lens, "new_lens", i32, (B,), dev), B,
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), max_pages,
                 _arg(free_pages, "free_pages", i32, (cap,), dev), cap, _arg(free_state, "free_state", i32, (2,), dev),
                 page_size, n_pages, max_tokens, _arg(r["seq_lens"], "seq_lens", i32, (B,), dev),
@@ -580,26 +612,30 @@ def paged_append(k, v, k_gamma, positions, slots, k_pages, v_pages, rope_base: f
     positions and slots int32 [T] (slot below 0: not cached), k_pages/v_pages bf16
     [n_pages,Hkv,page_size,D] (updated in place).
     """
+    if q_hat is None and stream is None:
+        r = (_quick or _load_quick()).paged_append(k, v, k_gamma, positions, slots, k_pages, v_pages, rope_base, interp_factor,
+                                                   q, q_gamma, status)
+        if r is not None:
+            return None if r is True else r
     torch = _torch()
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    T, Hkv, D = _dims(k, "k", bf16, 3)
-    pool = _dims(k_pages, "k_pages", bf16, 4)
-    n_pages, _, P, _ = pool
-    dev = k.device
+    kv = T, Hkv, D = _shape(k, "k", 3)
+    n_pages, _, P, _ = _shape(k_pages, "k_pages", 4)
+    pool = (n_pages, Hkv, P, D)
+    dev = _gpu_of(k, "k")
     Hq, pq, pg, ph = 0, None, None, None
     if q is not None:
-        Hq = _dims(q, "q", bf16, 3)[1]
-        if q_hat is None:
-            q_hat = _empty(stream, dev, (T, Hq, D), bf16)
+        Hq = _shape(q, "q", 3)[1]
         pq, pg = _arg(q, "q", bf16, (T, Hq, D), dev), _arg(q_gamma, "q_gamma", f32, (D,), dev)
+        if q_hat is None:
+            q_hat = _empty(stream, dev, bf16, T, Hq, D)
         ph = _arg(q_hat, "q_hat", bf16, (T, Hq, D), dev)
     elif q_gamma is not None or q_hat is not None:
         raise ValueError("q_gamma and q_hat are given with q only")
-    _paged_call("g3attn_paged_append", dev, stream, status, pq, k.data_ptr(), _arg(v, "v", bf16, (T, Hkv, D), dev), pg,
+    _paged_call("g3attn_paged_append", dev, stream, status, pq, _arg(k, "k", bf16, kv, dev), _arg(v, "v", bf16, kv, dev), pg,
                 _arg(k_gamma, "k_gamma", f32, (D,), dev), _arg(positions, "positions", i32, (T,), dev),
-                _arg(slots, "slots", i32, (T,), dev), _arg(k_pages, "k_pages", bf16, (n_pages, Hkv, P, D), dev),
-                _arg(v_pages, "v_pages", bf16, (n_pages, Hkv, P, D), dev), n_pages, P, rope_base, interp_factor, T, Hq,
-                Hkv, D, ph)
+                _arg(slots, "slots", i32, (T,), dev), _arg(k_pages, "k_pages", bf16, pool, dev),
+                _arg(v_pages, "v_pages", bf16, pool, dev), n_pages, P, rope_base, interp_factor, T, Hq, Hkv, D, ph)
     return q_hat
 
 
@@ -610,12 +646,14 @@ def page_bounds(k_pages, block_table, old_lens, seq_lens, bounds, exps, *, statu
     old_lens/seq_lens int32 [B]; bounds int8 [n_pages,Hkv,2,D] and exps int8
     [n_pages,Hkv], updated in place.
     """
+    if stream is None and (_quick or _load_quick()).page_bounds(k_pages, block_table, old_lens, seq_lens, bounds, exps, status):
+        return bounds, exps
     torch = _torch()
     i32, i8 = torch.int32, torch.int8
-    n_pages, Hkv, P, D = _dims(k_pages, "k_pages", torch.bfloat16, 4)
-    B, max_pages = _dims(block_table, "block_table", i32, 2)
-    dev = k_pages.device
-    _paged_call("g3attn_page_bounds", dev, stream, status, k_pages.data_ptr(),
+    pool = n_pages, Hkv, P, D = _shape(k_pages, "k_pages", 4)
+    B, max_pages = _shape(block_table, "block_table", 2)
+    dev = _gpu_of(k_pages, "k_pages")
+    _paged_call("g3attn_page_bounds", dev, stream, status, _arg(k_pages, "k_pages", torch.bfloat16, pool, dev),
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(old_lens, "old_lens", i32, (B,), dev),
                 _arg(seq_lens, "seq_lens", i32, (B,), dev), B, max_pages, n_pages, P, Hkv, D,
                 _arg(bounds, "bounds", i8, (n_pages, Hkv, 2, D), dev), _arg(exps, "exps", i8, (n_pages, Hkv), dev))
@@ -629,18 +667,22 @@ def page_select(q_hat, bounds, exps, block_table, seq_lens, page_size: int, n_se
     q_hat bf16 [B,Hq,D] from paged_append, bounds/exps from page_bounds; returns
     int32 [B,Hkv,n_select], for paged_decode(pages=...).
     """
+    if out is None and ws is None and stream is None:
+        r = (_quick or _load_quick()).page_select(q_hat, bounds, exps, block_table, seq_lens, page_size, n_select, status)
+        if r is not None:
+            return r
     torch = _torch()
     i32, i8 = torch.int32, torch.int8
-    B, Hq, D = _dims(q_hat, "q_hat", torch.bfloat16, 3)
-    n_pages, Hkv = _dims(exps, "exps", i8, 2)
-    _, max_pages = _dims(block_table, "block_table", i32, 2)
-    dev = q_hat.device
+    B, Hq, D = _shape(q_hat, "q_hat", 3)
+    n_pages, Hkv = _shape(exps, "exps", 2)
+    max_pages = _shape(block_table, "block_table", 2)[1]
+    dev = _gpu_of(q_hat, "q_hat")
     if out is None:
-        out = _empty(stream, dev, (B, Hkv, max(n_select, 0)), i32)
+        out = _empty(stream, dev, i32, B, Hkv, max(n_select, 0))
     if ws is None:
-        ws = _empty(stream, dev, (max(page_select_workspace_size(B, Hkv, max_pages), 1),), torch.uint8)
+        ws = _empty(stream, dev, torch.uint8, max(page_select_workspace_size(B, Hkv, max_pages), 1))
     ws, ws_bytes = _ws(ws, 0, dev)
-    _paged_call("g3attn_page_select", dev, stream, status, q_hat.data_ptr(),
+    _paged_call("g3attn_page_select", dev, stream, status, _arg(q_hat, "q_hat", torch.bfloat16, (B, Hq, D), dev),
                 _arg(bounds, "bounds", i8, (n_pages, Hkv, 2, D), dev), _arg(exps, "exps", i8, (n_pages, Hkv), dev),
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), B,
                 max_pages, n_pages, page_size, Hq, Hkv, D, n_select, _arg(out, "out", i32, (B, Hkv, n_select), dev),
@@ -657,25 +699,31 @@ def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int
     (the new token included; 0: idle, a zero row), pages int32 [B,Hkv,n] from
     page_select or None (all pages; the last `window` tokens on a LOCAL layer).
     """
+    if out is None and ws is None and stream is None:
+        r = (_quick or _load_quick()).paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind, window, pages,
+                                                   return_lse, status)
+        if r is not None:
+            return r
     torch = _torch()
     bf16, i32 = torch.bfloat16, torch.int32
-    B, Hq, D = _dims(q_hat, "q_hat", bf16, 3)
-    n_pages, Hkv, P, _ = _dims(k_pages, "k_pages", bf16, 4)
-    _, max_pages = _dims(block_table, "block_table", i32, 2)
-    dev = q_hat.device
+    B, Hq, D = _shape(q_hat, "q_hat", 3)
+    dev = _gpu_of(q_hat, "q_hat")
+    n_pages, Hkv, P, _ = _shape(k_pages, "k_pages", 4)
+    max_pages = _shape(block_table, "block_table", 2)[1]
     pool = (n_pages, Hkv, P, D)
     n_select, plist = 0, None
     if pages is not None:
-        n_select = _dims(pages, "pages", i32, 3)[2]
+        n_select = _shape(pages, "pages", 3)[2]
         plist = _arg(pages, "pages", i32, (B, Hkv, n_select), dev)
     if out is None:
-        out = _empty(stream, dev, (B, Hq, D), bf16)
-    lse = _empty(stream, dev, (B, Hq), torch.float32) if return_lse else None
+        out = _empty(stream, dev, bf16, B, Hq, D)
+    lse = _empty(stream, dev, torch.float32, B, Hq) if return_lse else None
     if ws is None:
-        ws = _empty(stream, dev, (max(paged_decode_workspace_size(B, D), 1),), torch.uint8)
+        ws = _empty(stream, dev, torch.uint8, max(paged_decode_workspace_size(B, D), 1))
     ws, ws_bytes = _ws(ws, 0, dev)
-    _paged_call("g3attn_paged_decode", dev, stream, status, q_hat.data_ptr(), _arg(k_pages, "k_pages", bf16, pool, dev),
-                _arg(v_pages, "v_pages", bf16, pool, dev), _arg(block_table, "block_table", i32, (B, max_pages), dev),
-                _arg(seq_lens, "seq_lens", i32, (B,), dev), plist, n_select, int(layer_kind), int(window), B, max_pages,
-                n_pages, P, Hq, Hkv, D, _arg(out, "out", bf16, (B, Hq, D), dev), _ptr(lse), ws.data_ptr(), ws_bytes)
+    _paged_call("g3attn_paged_decode", dev, stream, status, _arg(q_hat, "q_hat", bf16, (B, Hq, D), dev),
+                _arg(k_pages, "k_pages", bf16, pool, dev), _arg(v_pages, "v_pages", bf16, pool, dev),
+                _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), plist,
+                n_select, int(layer_kind), int(window), B, max_pages, n_pages, P, Hq, Hkv, D,
+                _arg(out, "out", bf16, (B, Hq, D), dev), _ptr(lse), ws.data_ptr(), ws_bytes)
     return (out, lse) if return_lse else out

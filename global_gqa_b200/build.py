@@ -1,4 +1,5 @@
-"""Builds libg3attn.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libg3attn.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_paged.so, the Python module that calls its paged-cache part.
 
 Usage: python -m global_gqa_b200.build  [--force] [--verbose]
 """
@@ -87,7 +88,49 @@ def build_fault_inject(force: bool = False) -> str:
     return FAULT_LIB
 
 
+BINDING = os.path.join(HERE, "_paged.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """The module that calls the library's paged-cache part from Python (csrc/binding.cpp), for this torch."""
+    import sysconfig
+
+    import torch
+    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "g3attn.h")
+    base = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), src, "-L", HERE, "-l:libg3attn.so",
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    h = hashlib.sha256((" ".join(cmd) + torch.__version__).encode())
+    for f in (src, header):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    stamp, dig = BINDING + ".sha256", h.hexdigest()
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == dig:
+                return BINDING
+    tmp = BINDING + ".tmp"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on binding.cpp")
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(dig)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_lib(force, verbose)
+    build_binding(force)
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     stamp = LIB + ".sha256"
     dig = _digest()
     if not force and os.path.exists(LIB) and os.path.exists(stamp):

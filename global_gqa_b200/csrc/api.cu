@@ -938,7 +938,14 @@ g3_status g3attn_paged_append(const void* q, const void* k, const void* v, const
   p.q_hat = static_cast<__nv_bfloat16*>(q_hat);
   p.status = status;
   p.interp = interp_factor;
-  for (int f = 0; f < D / 2; ++f) p.inv_freq[f] = std::exp(-2.0 * f / D * std::log((double)rope_base));
+  // A layer's frequencies depend on its base and head dim alone: this thread's last ones serve the next call too.
+  static thread_local struct { float base; int D; double inv_freq[128]; } last = {0.f, 0, {}};
+  if (last.base != rope_base || last.D != D) {
+    for (int f = 0; f < D / 2; ++f) last.inv_freq[f] = std::pow((double)rope_base, -2.0 * f / D);
+    last.base = rope_base;
+    last.D = D;
+  }
+  std::memcpy(p.inv_freq, last.inv_freq, (D / 2) * sizeof(double));
   p.T = T;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -992,6 +999,7 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
   if (!q_hat || !bounds || !exps || !block_table || !seq_lens || !pages)
     return fail(G3_ERR_INVALID_ARG, "page_select: a required pointer is NULL");
   if (n_select < 1) return fail(G3_ERR_INVALID_ARG, "page_select: n_select=%d", n_select);
+  if ((long long)B * Hkv > 0x7fffffffLL / 8) return fail(G3_ERR_UNSUPPORTED, "page_select: %d x %d pairs are too many", B, Hkv);
   g3_status s = check_pool("page_select", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
   if (s == G3_OK) s = check_group("page_select", Hq, Hkv);
   if (s != G3_OK) return s;
@@ -1020,10 +1028,8 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
   p.n_pages = n_pages;
   p.n_select = n_select;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = traced("page_scores", st, [&] { return g3::launch_page_scores(p, D, st); });
-  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_select scores: %s", cudaGetErrorString(e));
-  e = traced("page_pick", st, [&] { return g3::launch_page_pick(p, st); });
-  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_select pick: %s", cudaGetErrorString(e));
+  const cudaError_t e = traced("page_select", st, [&] { return g3::launch_page_select(p, D, st); });
+  if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_select: %s", cudaGetErrorString(e));
   return G3_OK;
 }
 

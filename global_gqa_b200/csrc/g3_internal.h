@@ -244,8 +244,7 @@ struct PageSelectParams {
   int* status;
   int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select;
 };
-cudaError_t launch_page_scores(const PageSelectParams& p, int D, cudaStream_t st);
-cudaError_t launch_page_pick(const PageSelectParams& p, cudaStream_t st);
+cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st);
 
 struct PagedDecodeParams {
   const __nv_bfloat16* q_hat;  // [B, Hq, D]

@@ -8,8 +8,8 @@
 //                   their slots, queries to a packed buffer.
 //   page_bounds   : feature-wise largest and smallest key of each page and kv
 //                   head, in 8 bits.
-//   page_scores   : an upper bound of q . k over each page's keys, from the bounds.
-//   page_pick     : the pages with the highest scores of each (sequence, kv head).
+//   page_select   : an upper bound of q . k over each page's keys, from the bounds,
+//                   and the pages with the highest ones of each (sequence, kv head).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -319,8 +319,9 @@ cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st) {
 }
 
 // ============================================================== page bounds
-// HBM-bound: one warp reads the rows of one (page, kv head) once, keeping the
-// largest and smallest value of 8 features per lane in packed bf16.
+// HBM-bound: the rows of one (page, kv head) are read once, by one warp or, with
+// few pages, by up to 8 that share them; a lane keeps the largest and smallest
+// value of 8 features in packed bf16.
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsUnroll = 8;  // 16-byte loads in flight per lane
 
@@ -334,9 +335,10 @@ __device__ __forceinline__ int bound_exponent(uint32_t bf16_bits) {
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
 
 template <int D>
-__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsParams p) {
+__global__ void __launch_bounds__(kBoundsThreads, 6) page_bounds_kernel(PageBoundsParams p) {
   extern __shared__ int bounds_smem[];  // [B + 1] touched pages before each sequence
   __shared__ int warp_sums[kBoundsThreads / 32];
+  __shared__ __nv_bfloat162 s_part[kBoundsThreads / 32][8][32];
   constexpr int LPT = D / 8;     // lanes per row
   constexpr int TPS = 32 / LPT;  // rows per warp-wide load
   griddep_wait();
@@ -351,21 +353,22 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsP
     return max(0, ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift));
   });
   const long long units = (long long)bounds_smem[p.B] * p.Hkv;
-  const int lane = threadIdx.x & 31, li = lane % LPT, sub = lane / LPT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LPT, sub = lane / LPT;
   const int P = 1 << p.page_shift;
-  for (long long u = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * (kBoundsThreads / 32)) {
-    const int pj = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
+  constexpr int WARPS = kBoundsThreads / 32;
+  int split = 1;  // warps that share a unit's rows
+  while (split < WARPS && units * split * 2 <= (long long)gridDim.x * WARPS && split * TPS * kBoundsUnroll < P) split *= 2;
+  const int part = warp % split;
+  for (long long u0 = (long long)blockIdx.x * (WARPS / split); u0 < units; u0 += (long long)gridDim.x * (WARPS / split)) {
+    const long long u = u0 + warp / split;
+    const int pj = (int)(min(u, units - 1) / p.Hkv), h = (int)(u % p.Hkv);
     const int b = find_row(bounds_smem, p.B, pj, 1);
     const int j = (p.old_lens[b] >> p.page_shift) + pj - bounds_smem[b];
-    const int rows = min(P, p.seq_lens[b] - (j << p.page_shift));
     const int page = p.block_table[(size_t)b * p.max_pages + j];
-    if (page < 0 || page >= p.n_pages) {
-      if (lane == 0) record_error(p.status, kErrInvalid, 321);
-      continue;
-    }
-    if (rows <= 0) continue;  // the old length at a page's end
-    const uint4* base = reinterpret_cast<const uint4*>(p.k_pages + ((((size_t)page * p.Hkv + h) << p.page_shift)) * D) + li;
+    const bool ok = u < units && page >= 0 && page < p.n_pages;
+    if (u < units && !ok && lane == 0) record_error(p.status, kErrInvalid, 321);
+    const int rows = ok ? min(P, p.seq_lens[b] - (j << p.page_shift)) : 0;
+    const uint4* base = reinterpret_cast<const uint4*>(p.k_pages + (((size_t)(ok ? page : 0) * p.Hkv + h) << p.page_shift) * D) + li;
     const __nv_bfloat162 ninf = __floats2bfloat162_rn(-INFINITY, -INFINITY), pinf = __floats2bfloat162_rn(INFINITY, INFINITY);
     __nv_bfloat162 mx[4], mn[4];
 #pragma unroll
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsP
       mx[i] = ninf;
       mn[i] = pinf;
     }
-    for (int r0 = 0; r0 < rows; r0 += TPS * kBoundsUnroll) {
+    for (int r0 = part * TPS * kBoundsUnroll; r0 < rows; r0 += split * TPS * kBoundsUnroll) {
       uint4 x[kBoundsUnroll];
 #pragma unroll
       for (int k = 0; k < kBoundsUnroll; ++k) {
@@ -398,6 +401,24 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsP
         mn[i] = __hmin2_nan(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
       }
     }
+    if (split > 1) {
+      __syncthreads();  // the last unit's parts have been read
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s_part[warp][i][lane] = mx[i];
+        s_part[warp][4 + i][lane] = mn[i];
+      }
+      __syncthreads();
+      if (part == 0) {
+        for (int w = 1; w < split; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mx[i] = __hmax2_nan(mx[i], s_part[warp + w][i][lane]);
+            mn[i] = __hmin2_nan(mn[i], s_part[warp + w][4 + i][lane]);
+          }
+      }
+    }
+    if (part != 0 || !ok) continue;
     // Bits of |x| of bf16 values order as integers; a NaN's are above infinity's.
     uint32_t amax = 0;
 #pragma unroll
@@ -435,7 +456,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(PageBoundsP
 
 cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st) {
   const long long most = ((long long)p.B * p.max_pages * p.Hkv + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
-  const dim3 grid((unsigned)std::min<long long>(most, 148 * 4)), block(kBoundsThreads);
+  const dim3 grid((unsigned)std::min<long long>(most, 148 * 6)), block(kBoundsThreads);
   const size_t smem = (p.B + 1) * sizeof(int);
   switch (D) {
     case 64: return launch_dependent(page_bounds_kernel<64>, grid, block, smem, st, p);
@@ -445,7 +466,7 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
   return cudaErrorInvalidValue;
 }
 
-// ============================================================== page scores
+// ============================================================== page select
 // score(b, kv head, page) = max over the group's query heads of
 //     2^-(eq + ek) * sum_d (q8_d >= 0 ? q8_d * max8_d : q8_d * min8_d),
 // with q8 = the query's features rounded to 8 bits with a power-of-two exponent
@@ -453,13 +474,17 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
 // numbers below 2^24 in any order, so the scores are exact and the selection does
 // not depend on how they are summed.  HBM-bound: 2D + 1 bytes per (page, kv head).
 //
-// One warp takes 64 pages of one (sequence, kv head), 16 at a time, as
+// A cluster of blocks takes one (sequence, kv head); the warps of each block bring
+// the group's queries to 8 bits, one head each, then score 16 pages at a time as
 // mma.m16n8k32 of 8-bit whole numbers: rows are pages, columns the group's heads.
 // Each lane loads 16-byte pieces of two pages' bounds straight into its A
 // fragments; the order of the features inside a product is free, so the pieces
-// are used as they come and the query is laid out to match.
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 64;  // pages of one warp task
+// are used as they come and the query is laid out to match.  Behind the cluster's
+// barrier its first block picks the pages: the scores as ordered integers, the
+// threshold by 8-bit digits below the highest bit in which they differ, then an
+// ordered write.
+constexpr int kSelectThreads = 256;
+constexpr int kSelectWarps = kSelectThreads / 32;
 
 __device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -468,157 +493,56 @@ __device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(PageSelectParams p) {
-  constexpr int WARPS = kScoreThreads / 32;
-  constexpr int PIECES = 2 * D / 64;  // 16-byte pieces of a page's bounds per lane
-  constexpr int FPL = D / 32;         // query features per lane
-  extern __shared__ int score_smem[];  // [B + 1] tasks before each sequence
-  __shared__ int warp_sums[WARPS];
-  __shared__ __align__(16) int8_t q8[WARPS][8][2 * D];
-  __shared__ float q_unit[WARPS][8];
-  griddep_wait();
-  griddep_launch();
-  const long long room = (long long)p.max_pages << p.page_shift;
-  block_prefix(p.B, score_smem, warp_sums, [&](int b) {
-    const int L = p.seq_lens[b];
-    if (L < 0 || L > room) {
-      if (blockIdx.x == 0) record_error(p.status, kErrInvalid, 330);
-      return 0;
-    }
-    const int np = (L + (1 << p.page_shift) - 1) >> p.page_shift;
-    return np <= p.n_select ? 0 : (np + kScorePages - 1) / kScorePages;  // no choice, no scores
-  });
-  const long long tasks = (long long)score_smem[p.B] * p.Hkv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = lane >> 2, c = lane & 3;
-  for (long long u = (long long)blockIdx.x * WARPS + warp; u < tasks; u += (long long)gridDim.x * WARPS) {
-    const int tj = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
-    const int b = find_row(score_smem, p.B, tj, 1);
-    const int page0 = (tj - score_smem[b]) * kScorePages;
-    const int np = (p.seq_lens[b] + (1 << p.page_shift) - 1) >> p.page_shift;
-    // Physical pages of the task's 64 (the pages past the last one repeat it).
-    int ids[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = min(page0 + 32 * i + lane, np - 1);
-      int id = p.block_table[(size_t)b * p.max_pages + j];
-      if (id < 0 || id >= p.n_pages) {
-        record_error(p.status, kErrInvalid, 331);
-        id = -1;
-      }
-      ids[i] = id;
-    }
-    // The group's queries in 8 bits: positive parts, then negative parts.
-    __syncwarp();
-    for (int g = 0; g < 8; ++g) {
-      float x[FPL];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int i = 0; i < FPL; ++i) {
-        x[i] = g < p.G ? __bfloat162float(p.q_hat[((size_t)b * p.Hq + h * p.G + g) * D + i * 32 + lane]) : 0.f;
-        if (x[i] != x[i]) x[i] = 0.f;
-        amax = max(amax, (__float_as_uint(x[i]) & 0x7fffffffu) >> 16);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-      const int e = bound_exponent(amax);
-      const float unit = exp2_int(e);
-#pragma unroll
-      for (int i = 0; i < FPL; ++i) {
-        const int v = (int)fminf(fmaxf(rintf(x[i] * unit), -127.f), 127.f);
-        q8[warp][g][i * 32 + lane] = (int8_t)max(v, 0);
-        q8[warp][g][D + i * 32 + lane] = (int8_t)min(v, 0);
-      }
-      if (lane == 0) q_unit[warp][g] = exp2_int(-e);
-    }
-    __syncwarp();
-    uint4 bq[PIECES];
-#pragma unroll
-    for (int k = 0; k < PIECES; ++k) bq[k] = *reinterpret_cast<const uint4*>(&q8[warp][row][c * 16 + 64 * k]);
-    const float unit0 = q_unit[warp][2 * c], unit1 = q_unit[warp][2 * c + 1];
-    float* dst = p.scores + ((size_t)b * p.Hkv + h) * p.max_pages;
-#pragma unroll
-    for (int grp = 0; grp < kScorePages / 16; ++grp) {
-      const int j0 = page0 + grp * 16;
-      if (j0 >= np) break;
-      const int id0 = __shfl_sync(0xffffffffu, ids[grp / 2], (grp % 2) * 16 + row);
-      const int id1 = __shfl_sync(0xffffffffu, ids[grp / 2], (grp % 2) * 16 + row + 8);
-      const size_t ph0 = (size_t)max(id0, 0) * p.Hkv + h, ph1 = (size_t)max(id1, 0) * p.Hkv + h;
-      const uint4* s0 = reinterpret_cast<const uint4*>(p.bounds + ph0 * 2 * D) + c;
-      const uint4* s1 = reinterpret_cast<const uint4*>(p.bounds + ph1 * 2 * D) + c;
-      uint4 a0[PIECES], a1[PIECES];
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        a0[k] = __ldg(s0 + 4 * k);
-        a1[k] = __ldg(s1 + 4 * k);
-      }
-      const int e0 = p.exps[ph0], e1 = p.exps[ph1];
-      int acc[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, bq[k].x, bq[k].y);
-        mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, bq[k].z, bq[k].w);
-      }
-      // acc: page row / row + 8, heads 2c and 2c + 1.
-      const float x0 = 2 * c < p.G ? (float)acc[0] * unit0 : -INFINITY, x1 = 2 * c + 1 < p.G ? (float)acc[1] * unit1 : -INFINITY;
-      const float y0 = 2 * c < p.G ? (float)acc[2] * unit0 : -INFINITY, y1 = 2 * c + 1 < p.G ? (float)acc[3] * unit1 : -INFINITY;
-      float s_lo = fmaxf(x0, x1) * exp2_int(-e0), s_hi = fmaxf(y0, y1) * exp2_int(-e1);
-#pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        s_lo = fmaxf(s_lo, __shfl_xor_sync(0xffffffffu, s_lo, off));
-        s_hi = fmaxf(s_hi, __shfl_xor_sync(0xffffffffu, s_hi, off));
-      }
-      if (c == 0) {  // a page with no valid id is chosen last
-        if (j0 + row < np) dst[j0 + row] = id0 < 0 ? -INFINITY : s_lo;
-        if (j0 + row + 8 < np) dst[j0 + row + 8] = id1 < 0 ? -INFINITY : s_hi;
-      }
-    }
-  }
-}
-
-// ================================================================ page pick
-// The newest page and the n_select - 1 highest scores of the others, equal
-// scores by the lower page, in ascending order.  One block per (sequence, kv
-// head): the scores as ordered integers, the threshold by four 8-bit digits,
-// then an ordered write.
-constexpr int kPickThreads = 256;
-
 // Ascending order of the floats (no NaN) as ascending unsigned integers; -0 counts as +0.
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParams p) {
-  constexpr int WARPS = kPickThreads / 32;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_left;
-  __shared__ int s_gt[WARPS], s_eq[WARPS];
-  griddep_wait();
-  griddep_launch();
+struct PickSmem {
+  uint32_t hist[256];
+  uint32_t digit, left, count;
+  uint32_t lo[kSelectWarps], hi[kSelectWarps];
+  int gt[kSelectWarps], eq[kSelectWarps];
+};
+
+// The k highest of n scores (0 < k < n), equal ones by the lower index, in
+// ascending order of the index, by the whole block.
+__device__ __forceinline__ void pick_pages(const float* sc, int n, int k, int32_t* out, PickSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int L = p.seq_lens[b];
-  const long long room = (long long)p.max_pages << p.page_shift;
-  const int np = L < 0 || L > room ? 0 : (L + (1 << p.page_shift) - 1) >> p.page_shift;
-  int32_t* out = p.pages + ((size_t)b * p.Hkv + h) * p.n_select;
-  if (np <= p.n_select) {
-    for (int i = tid; i < p.n_select; i += kPickThreads) out[i] = i < np ? i : -1;
-    return;
+  // Scores come from other blocks: read them where they are written, in L2.
+  auto key = [&](int i) { return ordered_bits(__ldcg(sc + i)); };
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for (int i = tid; i < n; i += kSelectThreads) {
+    const uint32_t u = key(i);
+    lo = min(lo, u);
+    hi = max(hi, u);
   }
-  const int k = p.n_select - 1, n = np - 1;  // k of the n pages before the newest
-  if (tid == 0) out[k] = n;
-  if (k == 0) return;
-  const float* sc = p.scores + ((size_t)b * p.Hkv + h) * p.max_pages;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  if (lane == 0) {
+    sm.lo[warp] = lo;
+    sm.hi[warp] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) {
+    lo = min(lo, sm.lo[w]);
+    hi = max(hi, sm.hi[w]);
+  }
+  // (key - lo) >> shift of the k-th highest is `prefix`; `left` of the scores with that prefix are taken.
   uint32_t prefix = 0, left = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
+  int shift = 32 - __clz(hi - lo);
+  while (shift > 0) {
+    const int next = max(shift - 8, 0), bits = shift - next;
+    sm.hist[tid] = 0;
     __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = tid; i < n; i += kPickThreads) {
-      const uint32_t u = ordered_bits(sc[i]);
-      if ((u & above) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+    for (int i = tid; i < n; i += kSelectThreads) {
+      const uint32_t u = key(i) - lo;
+      if (shift == 32 || (u >> shift) == prefix) atomicAdd(&sm.hist[(u >> next) & ((1u << bits) - 1u)], 1u);
     }
     __syncthreads();
     if (warp == 0) {
@@ -626,7 +550,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParam
       uint32_t d[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = hist[255 - (lane * 8 + i)];
+        d[i] = sm.hist[255 - (lane * 8 + i)];
         sum += d[i];
       }
       uint32_t inc = sum;
@@ -637,27 +561,29 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParam
       }
       uint32_t before = inc - sum;
       if (before < left && inc >= left) {
+        bool found = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (before < left && before + d[i] >= left) {
-            s_prefix = prefix | (uint32_t)(255 - (lane * 8 + i)) << shift;
-            s_left = left - before;
-            before = left;  // found
-          } else {
-            before += d[i];
+          if (!found && before + d[i] >= left) {
+            sm.digit = 255 - (lane * 8 + i);
+            sm.left = left - before;
+            sm.count = d[i];
+            found = true;
           }
+          before += d[i];
         }
       }
     }
     __syncthreads();
-    prefix = s_prefix;
-    left = s_left;
+    prefix = (shift == 32 ? 0u : prefix << bits) | sm.digit;
+    left = sm.left;
+    shift = next;
+    if (sm.count == left) break;  // all of them are taken: no finer threshold is needed
   }
-  // `prefix` is the k-th highest score; `left` of the pages that have it are taken.
-  const int per = ((n + WARPS - 1) / WARPS + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
+  const int per = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
   int gt = 0, eq = 0;
   for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t u = ordered_bits(sc[i]);
+    const uint32_t u = (key(i) - lo) >> shift;
     gt += u > prefix;
     eq += u == prefix;
   }
@@ -667,19 +593,20 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParam
     eq += __shfl_xor_sync(0xffffffffu, eq, off);
   }
   if (lane == 0) {
-    s_gt[warp] = gt;
-    s_eq[warp] = eq;
+    sm.gt[warp] = gt;
+    sm.eq[warp] = eq;
   }
   __syncthreads();
   int gt0 = 0, eq0 = 0;
   for (int w = 0; w < warp; ++w) {
-    gt0 += s_gt[w];
-    eq0 += s_eq[w];
+    gt0 += sm.gt[w];
+    eq0 += sm.eq[w];
   }
   const uint32_t below = (1u << lane) - 1u;
   for (int i = i0; i < i1; i += 32) {
-    const uint32_t u = i + lane < i1 ? ordered_bits(sc[i + lane]) : 0u;
-    const bool is_gt = i + lane < i1 && u > prefix, is_eq = i + lane < i1 && u == prefix;
+    const bool in = i + lane < i1;
+    const uint32_t u = in ? (key(i + lane) - lo) >> shift : 0u;
+    const bool is_gt = in && u > prefix, is_eq = in && u == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     const int eq_rank = eq0 + __popc(be & below);
     const int at = gt0 + __popc(bg & below) + min(eq_rank, (int)left);
@@ -689,20 +616,141 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(PageSelectParam
   }
 }
 
-cudaError_t launch_page_scores(const PageSelectParams& p, int D, cudaStream_t st) {
-  const long long most = ((long long)p.B * ((p.max_pages + kScorePages - 1) / kScorePages) * p.Hkv + 7) / 8;
-  const dim3 grid((unsigned)std::min<long long>(most, 148 * 4)), block(kScoreThreads);
-  const size_t smem = (p.B + 1) * sizeof(int);
-  switch (D) {
-    case 64: return launch_dependent(page_scores_kernel<64>, grid, block, smem, st, p);
-    case 128: return launch_dependent(page_scores_kernel<128>, grid, block, smem, st, p);
-    case 256: return launch_dependent(page_scores_kernel<256>, grid, block, smem, st, p);
+template <int D>
+__global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_kernel(PageSelectParams p) {
+  constexpr int PIECES = 2 * D / 64;  // 16-byte pieces of a page's bounds per lane
+  constexpr int FPL = D / 32;         // query features per lane
+  constexpr int QROW = 2 * D + 64;    // bytes from one head's row to the next: 16-byte reads of 8 rows without conflicts
+  __shared__ __align__(16) int8_t q8[8 * QROW];
+  __shared__ float q_unit[8];
+  __shared__ PickSmem pick;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = lane >> 2, c = lane & 3;
+  const int ranks = cluster_size(), rank = blockIdx.x % ranks;
+  const int pair = blockIdx.x / ranks, b = pair / p.Hkv, h = pair % p.Hkv;
+  griddep_wait();
+  griddep_launch();
+  const int L = p.seq_lens[b];
+  // The group's queries are on their way while the length is read.
+  float x[FPL];
+#pragma unroll
+  for (int i = 0; i < FPL; ++i)
+    x[i] = warp < p.G ? __bfloat162float(p.q_hat[((size_t)b * p.Hq + h * p.G + warp) * D + i * 32 + lane]) : 0.f;
+  const bool valid = L >= 0 && L <= (long long)p.max_pages << p.page_shift;
+  if (!valid && rank == 0 && tid == 0) record_error(p.status, kErrInvalid, 330);
+  const int np = valid ? (L + (1 << p.page_shift) - 1) >> p.page_shift : 0;
+  int32_t* out = p.pages + (size_t)pair * p.n_select;
+  if (np <= p.n_select) {  // no choice (the same for the whole cluster)
+    if (rank == 0)
+      for (int i = tid; i < p.n_select; i += kSelectThreads) out[i] = i < np ? i : -1;
+    return;
   }
-  return cudaErrorInvalidValue;
+  float* scores = p.scores + (size_t)pair * p.max_pages;
+  {
+    // 8 bits: positive parts, then negative parts.
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < FPL; ++i) {
+      if (x[i] != x[i]) x[i] = 0.f;
+      amax = max(amax, (__float_as_uint(x[i]) & 0x7fffffffu) >> 16);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const int e = bound_exponent(amax);
+    const float unit = exp2_int(e);
+#pragma unroll
+    for (int i = 0; i < FPL; ++i) {
+      const int v = (int)fminf(fmaxf(rintf(x[i] * unit), -127.f), 127.f);
+      q8[warp * QROW + i * 32 + lane] = (int8_t)max(v, 0);
+      q8[warp * QROW + D + i * 32 + lane] = (int8_t)min(v, 0);
+    }
+    if (lane == 0) q_unit[warp] = exp2_int(-e);
+  }
+  __syncthreads();
+  const float unit0 = q_unit[2 * c], unit1 = q_unit[2 * c + 1];
+  const bool has0 = 2 * c < p.G, has1 = 2 * c + 1 < p.G;
+  const int32_t* table = p.block_table + (size_t)b * p.max_pages;
+  const int step = ranks * kSelectWarps * 16;
+  int j0 = (rank * kSelectWarps + warp) * 16;
+  int id0 = 0, id1 = 0;
+  if (j0 < np) {
+    id0 = table[min(j0 + row, np - 1)];
+    id1 = table[min(j0 + row + 8, np - 1)];
+  }
+  for (; j0 < np; j0 += step) {
+    // Physical pages of rows `row` and `row + 8` (past the last page it is repeated); a bad one scores -infinity.
+    const bool bad0 = id0 < 0 || id0 >= p.n_pages, bad1 = id1 < 0 || id1 >= p.n_pages;
+    if (bad0 || bad1) record_error(p.status, kErrInvalid, 331);
+    const size_t ph0 = (size_t)(bad0 ? 0 : id0) * p.Hkv + h, ph1 = (size_t)(bad1 ? 0 : id1) * p.Hkv + h;
+    const uint4* s0 = reinterpret_cast<const uint4*>(p.bounds + ph0 * 2 * D) + c;
+    const uint4* s1 = reinterpret_cast<const uint4*>(p.bounds + ph1 * 2 * D) + c;
+    uint4 a0[PIECES], a1[PIECES];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      a0[k] = __ldg(s0 + 4 * k);
+      a1[k] = __ldg(s1 + 4 * k);
+    }
+    const int e0 = p.exps[ph0], e1 = p.exps[ph1];
+    if (j0 + step < np) {
+      id0 = table[min(j0 + step + row, np - 1)];
+      id1 = table[min(j0 + step + row + 8, np - 1)];
+    }
+    int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const uint4 bq = *reinterpret_cast<const uint4*>(&q8[row * QROW + c * 16 + 64 * k]);
+      mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, bq.x, bq.y);
+      mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, bq.z, bq.w);
+    }
+    // acc: page row / row + 8, heads 2c and 2c + 1.
+    float s_lo = fmaxf(has0 ? (float)acc[0] * unit0 : -INFINITY, has1 ? (float)acc[1] * unit1 : -INFINITY) * exp2_int(-e0);
+    float s_hi = fmaxf(has0 ? (float)acc[2] * unit0 : -INFINITY, has1 ? (float)acc[3] * unit1 : -INFINITY) * exp2_int(-e1);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      s_lo = fmaxf(s_lo, __shfl_xor_sync(0xffffffffu, s_lo, off));
+      s_hi = fmaxf(s_hi, __shfl_xor_sync(0xffffffffu, s_hi, off));
+    }
+    if (c == 0) {
+      if (j0 + row < np) scores[j0 + row] = bad0 ? -INFINITY : s_lo;
+      if (j0 + row + 8 < np) scores[j0 + row + 8] = bad1 ? -INFINITY : s_hi;
+    }
+  }
+  cluster_arrive();  // releases the scores to the cluster
+  if (rank != 0) return;
+  cluster_wait();
+  if (tid == 0) out[p.n_select - 1] = np - 1;
+  if (p.n_select > 1) pick_pages(scores, np - 1, p.n_select - 1, out, pick);
 }
 
-cudaError_t launch_page_pick(const PageSelectParams& p, cudaStream_t st) {
-  return launch_dependent(page_pick_kernel, dim3(p.Hkv, p.B), dim3(kPickThreads), 0, st, p);
+template <int D>
+static cudaError_t launch_select_d(const PageSelectParams& p, cudaStream_t st) {
+  const long long pairs = (long long)p.B * p.Hkv;
+  // Blocks per pair: up to 8 while they find a place at once, at least 16 pages for each of their warps.
+  int ranks = 1;
+  while (ranks < 8 && (long long)ranks * kSelectWarps * 16 < p.max_pages && pairs * ranks < 148 * 8) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * ranks));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, page_select_kernel<D>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_select_d<64>(p, st);
+    case 128: return launch_select_d<128>(p, st);
+    case 256: return launch_select_d<256>(p, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace g3

@@ -18,6 +18,16 @@ namespace g3 {
 // dependent, take its place on the SMs early; it still waits for this one's end.
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+__device__ __forceinline__ int cluster_size() {
+  int n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+// The cluster's barrier in two halves: what a thread wrote before its arrival is
+// visible to those that have waited.  A block that only arrives may end.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Inclusive prefix sums of count(b), b < n, into pref[1 .. n], pref[0] = 0, by
 // the whole block (a multiple of 32 threads; `warp_sums` holds one int per
 // warp).  Every block of a grid repeats it: a few microseconds at the largest n,

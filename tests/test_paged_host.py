@@ -8,9 +8,9 @@ import global_gqa_b200 as g3
 FAKE = 0x100000  # never dereferenced: every call below fails validation first
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def lib():
-    if not os.path.exists(g3.LIB_PATH):
+    if not os.path.exists(g3.LIB_PATH) or not os.path.exists(os.path.join(g3.HERE, "_paged.so")):
         from global_gqa_b200 import build
         build.build()
     return g3.lib()
