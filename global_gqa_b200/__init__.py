@@ -64,7 +64,7 @@ _SIGS = {
     "g3attn_page_select_workspace_size": (_sz, [_i32] * 3),
     "g3attn_page_select": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp,
                                           _vp, _sz, _vp, _vp]),
-    "g3attn_paged_decode_workspace_size": (_sz, [_i32] * 2),
+    "g3attn_paged_decode_workspace_size": (_sz, [_i32]),
     "g3attn_paged_decode": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, ctypes.c_int, _i32, _i32, _i32, _i32,
                                            _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "g3attn_check_device_error": (ctypes.c_int, [_vp, _vp]),
@@ -564,8 +564,8 @@ def page_select_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
     return int(lib().g3attn_page_select_workspace_size(B, Hkv, max_pages))
 
 
-def paged_decode_workspace_size(B: int, D: int) -> int:
-    return int(lib().g3attn_paged_decode_workspace_size(B, D))
+def paged_decode_workspace_size(D: int) -> int:
+    return int(lib().g3attn_paged_decode_workspace_size(D))
 
 
 def page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size: int, n_pages: int, max_tokens: int, *,
@@ -719,7 +719,7 @@ def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int
         out = _empty(stream, dev, bf16, B, Hq, D)
     lse = _empty(stream, dev, torch.float32, B, Hq) if return_lse else None
     if ws is None:
-        ws = _empty(stream, dev, torch.uint8, max(paged_decode_workspace_size(B, D), 1))
+        ws = _empty(stream, dev, torch.uint8, max(paged_decode_workspace_size(D), 1))
     ws, ws_bytes = _ws(ws, 0, dev)
     _paged_call("g3attn_paged_decode", dev, stream, status, _arg(q_hat, "q_hat", bf16, (B, Hq, D), dev),
                 _arg(k_pages, "k_pages", bf16, pool, dev), _arg(v_pages, "v_pages", bf16, pool, dev),

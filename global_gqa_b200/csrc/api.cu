@@ -844,9 +844,9 @@ static g3_status check_pool(const char* who, int32_t B, int32_t max_pages, int32
     return fail(G3_ERR_UNSUPPORTED, "%s: B=%d sequences, at most %d are built", who, B, g3::kPagedMaxSeqs);
   if ((long long)n_pages * page_size > 0x7fffffffLL)
     return fail(G3_ERR_UNSUPPORTED, "%s: %d pages of %d tokens: slots must fit in 31 bits", who, n_pages, page_size);
-  if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)B * max_pages * (page_size / 16) > 0x7fffffffLL)
-    return fail(G3_ERR_UNSUPPORTED, "%s: a block table of %d x %d pages is too large", who, B, max_pages);
-  if (Hkv > 0xffff) return fail(G3_ERR_UNSUPPORTED, "%s: Hkv=%d too large", who, Hkv);
+  if ((long long)max_pages * page_size > 0x7fffffffLL || Hkv > 0xffff ||
+      (long long)B * Hkv > 0x7fffffffLL / ((long long)max_pages * (page_size / 16)))
+    return fail(G3_ERR_UNSUPPORTED, "%s: a block table of %d x %d pages with %d kv heads is too large", who, B, max_pages, Hkv);
   return G3_OK;
 }
 static g3_status check_group(const char* who, int32_t Hq, int32_t Hkv) {
@@ -1035,22 +1035,21 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
 
 namespace {
 struct PagedDecodeWs {
-  size_t pref, part_ml, part_o, total;
+  size_t cuts, part_ml, part_o, total;
 };
-PagedDecodeWs paged_decode_ws(int B, int D) {
+PagedDecodeWs paged_decode_ws(int D) {
   PagedDecodeWs w;
-  const size_t slots = 2 * (size_t)g3::paged_decode_blocks(D);
-  w.pref = 0;
-  w.part_ml = align_up(((size_t)B + 1) * 4, 256);
-  w.part_o = align_up(w.part_ml + slots * 8 * 2 * 4, 256);
-  w.total = w.part_o + slots * 8 * D * 4;
+  const size_t blocks = g3::paged_decode_blocks(D);
+  w.cuts = 0;
+  w.part_ml = align_up(blocks * sizeof(int4), 256);
+  w.part_o = align_up(w.part_ml + 2 * blocks * 8 * 2 * 4, 256);
+  w.total = w.part_o + 2 * blocks * 8 * D * 4;
   return w;
 }
 }  // namespace
 
-size_t g3attn_paged_decode_workspace_size(int32_t B, int32_t D) {
-  if (B < 1 || B > g3::kPagedMaxSeqs || !supported_d(D)) return 0;
-  return paged_decode_ws(B, D).total;
+size_t g3attn_paged_decode_workspace_size(int32_t D) {
+  return supported_d(D) ? paged_decode_ws(D).total : 0;
 }
 
 g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -1071,11 +1070,9 @@ g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void
   g3_status s = check_pool("paged_decode", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
   if (s == G3_OK) s = check_group("paged_decode", Hq, Hkv);
   if (s != G3_OK) return s;
-  if ((long long)B * std::min(n_select, max_pages) * (page_size / 16) > 0x7fffffffLL)
-    return fail(G3_ERR_UNSUPPORTED, "paged_decode: too many selected pages");
   if (!aligned16(q_hat) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return fail(G3_ERR_INVALID_ARG, "paged_decode: q_hat, the pages and out must be 16-byte aligned");
-  const PagedDecodeWs w = paged_decode_ws(B, D);
+  const PagedDecodeWs w = paged_decode_ws(D);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(G3_ERR_WORKSPACE, "paged_decode: workspace NULL or not 256-byte aligned");
   if (workspace_bytes < w.total)
@@ -1091,7 +1088,7 @@ g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.status = status;
-  p.pref = reinterpret_cast<int32_t*>(ws + w.pref);
+  p.cuts = reinterpret_cast<int4*>(ws + w.cuts);
   p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.B = B;
@@ -1105,6 +1102,9 @@ g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void
   p.kind = (int)layer_kind;
   p.window = window;
   p.n_blocks = g3::paged_decode_blocks(D);
+// With 8 or more blocks per pair, the unequal shares of dealt blocks (at most an eighth) cost less than
+  // a block's second pass for the pair it shares with its neighbour (2 of 11 us at one sequence of 4K tokens).
+  p.deal = (long long)B * Hkv * 8 <= p.n_blocks ? 1 : 0;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced("paged_decode", st, [&] { return g3::launch_paged_decode(p, D, st); });

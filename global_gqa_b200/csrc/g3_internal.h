@@ -217,7 +217,7 @@ struct PagedAppendParams {
   double interp;
   double inv_freq[128];  // base^(-2f/D), f < D/2
   int T, Hq, Hkv, page_shift, n_slots;
-  int warps_per_token;  // set by the launcher
+  int warps_shift;  // set by the launcher: 2^warps_shift warps share a token's rows
 };
 cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st);
 
@@ -256,11 +256,14 @@ struct PagedDecodeParams {
   __nv_bfloat16* out;    // [B, Hq, D]
   float* lse;            // [B, Hq] or null
   int* status;
-  int32_t* pref;   // [B + 1]: units before each sequence, from the decode kernel to the combine
+  // Pairs that were cut: pair (-1: none), first and last block, slot of the first part.  [n_blocks] by the block
+  // that begins them, or by pair where blocks are dealt.
+  int4* cuts;
   float* part_ml;  // [2 * n_blocks, 8, 2] (max, sum) in log2 units
   float* part_o;   // [2 * n_blocks, 8, D]
   int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select, kind, window;
   int n_blocks;
+  int deal;  // blocks are dealt to the pairs
   float scale_log2;
 };
 int paged_decode_blocks(int D);

@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
 
   // A granted request's fresh page i (0-based among its own) or -1.
   auto fresh_page = [&](int asked_before, int i) {
-    const int id = p.free_pages[((long long)head + asked_before + i) % p.free_cap];
+    const uint32_t at = (uint32_t)head + (uint32_t)(asked_before + i);  // both parts are below free_cap
+    const int id = p.free_pages[at < (uint32_t)p.free_cap ? at : at - (uint32_t)p.free_cap];
     return id >= 0 && id < p.n_pages ? id : -1;
   };
 
@@ -211,11 +212,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
     gam[i] = i >= D ? p.k_gamma[i - D] : p.Hq > 0 ? p.q_gamma[i] : 0.f;
   __syncthreads();
 
-  // `share` of a token's rows: warps_per_token warps split them.
-  const long long items = (long long)p.T * p.warps_per_token;
+  // `share` of a token's rows: 2^warps_shift warps split them.
+  const int warps_per_token = 1 << p.warps_shift;
+  const long long items = (long long)p.T << p.warps_shift;
   const long long stride = (long long)gridDim.x * (kAppendThreads / 32);
   for (long long it = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); it < items; it += stride) {
-    const int t = (int)(it / p.warps_per_token), share = (int)(it % p.warps_per_token);
+    const int t = (int)(it >> p.warps_shift), share = (int)it & (warps_per_token - 1);
     const int slot = p.slots[t];
     const bool keep = slot >= 0 && slot < p.n_slots;
     if (slot >= p.n_slots && lane == 0 && share == 0) record_error(p.status, kErrInvalid, 310);
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
     const size_t crow0 = ((page * p.Hkv) << p.page_shift) + (keep ? slot & ((1 << p.page_shift) - 1) : 0);
     const __nv_bfloat16* qrow = p.q + (size_t)t * p.Hq * D;
     const __nv_bfloat16* krow = p.k + (size_t)t * p.Hkv * D;
-    for (int h0 = share * RPW * kAppendUnroll; h0 < heads; h0 += p.warps_per_token * RPW * kAppendUnroll) {
+    for (int h0 = share * RPW * kAppendUnroll; h0 < heads; h0 += warps_per_token * RPW * kAppendUnroll) {
       uint4 xa[kAppendUnroll], xb[kAppendUnroll];
 #pragma unroll
       for (int u = 0; u < kAppendUnroll; ++u) {
@@ -305,10 +307,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
 cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st) {
   // A few tokens: split each one's rows over more warps, up to one step of rows each.
   const int rows_step = 32 / (D / 16) * kAppendUnroll, heads = p.Hq + p.Hkv;
-  p.warps_per_token = 1;
-  while (p.warps_per_token < 8 && p.warps_per_token * rows_step < heads && (long long)p.T * p.warps_per_token < 148 * 16)
-    p.warps_per_token *= 2;
-  const long long items = (long long)p.T * p.warps_per_token;
+  p.warps_shift = 0;
+  while (p.warps_shift < 3 && (rows_step << p.warps_shift) < heads && ((long long)p.T << p.warps_shift) < 148 * 16) ++p.warps_shift;
+  const long long items = (long long)p.T << p.warps_shift;
   const unsigned blocks = (unsigned)std::min<long long>((items + kAppendThreads / 32 - 1) / (kAppendThreads / 32), 148 * 8);
   switch (D) {
     case 64: return launch_dependent(paged_append_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
@@ -352,16 +353,15 @@ __global__ void __launch_bounds__(kBoundsThreads, 6) page_bounds_kernel(PageBoun
     }
     return max(0, ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift));
   });
-  const long long units = (long long)bounds_smem[p.B] * p.Hkv;
+  const int units = bounds_smem[p.B] * p.Hkv;  // below 2^31: checked on the host for the widest table
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LPT, sub = lane / LPT;
   const int P = 1 << p.page_shift;
   constexpr int WARPS = kBoundsThreads / 32;
   int split = 1;  // warps that share a unit's rows
-  while (split < WARPS && units * split * 2 <= (long long)gridDim.x * WARPS && split * TPS * kBoundsUnroll < P) split *= 2;
+  while (split < WARPS && units <= (int)gridDim.x * WARPS / (2 * split) && split * TPS * kBoundsUnroll < P) split *= 2;
   const int part = warp % split;
-  for (long long u0 = (long long)blockIdx.x * (WARPS / split); u0 < units; u0 += (long long)gridDim.x * (WARPS / split)) {
-    const long long u = u0 + warp / split;
-    const int pj = (int)(min(u, units - 1) / p.Hkv), h = (int)(u % p.Hkv);
+  for (int u0 = blockIdx.x * (WARPS / split); u0 < units; u0 += gridDim.x * (WARPS / split)) {
+    const int u = u0 + warp / split, pj = min(u, units - 1) / p.Hkv, h = u % p.Hkv;
     const int b = find_row(bounds_smem, p.B, pj, 1);
     const int j = (p.old_lens[b] >> p.page_shift) + pj - bounds_smem[b];
     const int page = p.block_table[(size_t)b * p.max_pages + j];

@@ -57,12 +57,12 @@ __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F
   __syncthreads();
 }
 
-// The b with pref[b] * scale <= x < pref[b + 1] * scale; 0 <= x < pref[n] * scale.
-__device__ __forceinline__ int find_row(const int* pref, int n, long long x, int scale) {
+// The b with pref[b] * scale <= x < pref[b + 1] * scale; 0 <= x < pref[n] * scale < 2^31.
+__device__ __forceinline__ int find_row(const int* pref, int n, int x, int scale) {
   int lo = 0, hi = n;  // pref[lo] * scale <= x < pref[hi] * scale
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((long long)pref[mid] * scale <= x)
+    if (pref[mid] * scale <= x)
       lo = mid;
     else
       hi = mid;

@@ -413,7 +413,7 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
                              void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Bytes of workspace g3attn_paged_decode needs (0 if the sizes are invalid); 256-byte aligned. */
-size_t g3attn_paged_decode_workspace_size(int32_t B, int32_t D);
+size_t g3attn_paged_decode_workspace_size(int32_t D);
 
 /*
  * Attention of one new token per sequence over its pages (steps 3 and 4 above).
@@ -426,7 +426,7 @@ size_t g3attn_paged_decode_workspace_size(int32_t B, int32_t D);
  *              logical pages only, as page_select gives them (ascending; -1
  *              pads the end).  NULL with n_select = 0: to all
  *   out        bf16 [B, Hq, D];  lse optional fp32 [B, Hq] (natural log, as prefill's)
- *   workspace  >= g3attn_paged_decode_workspace_size(B, D) bytes
+ *   workspace  >= g3attn_paged_decode_workspace_size(D) bytes (for any B and lengths)
  * A sequence that sees nothing (idle, or a length out of range, which is
  * recorded) gets a zero row and an lse of -infinity.  A page number out of
  * range, or a list entry that is out of range or not above the one before it,

@@ -346,6 +346,15 @@ def test_paged_decode_all(D, Hkv, G, P):
     assert clean()
 
 
+@pytest.mark.parametrize("D,Hkv,G,P", [(64, 8, 1, 16), (128, 16, 2, 32), (256, 8, 4, 16)])
+def test_paged_decode_many_short(D, Hkv, G, P):
+    """Pairs that are small parts of a block's share, beside idle sequences and one long one."""
+    lens = np.random.default_rng(D).integers(0, 40, 1500)
+    lens[::7], lens[700] = 0, 1200
+    run_decode(decode_case(lens, Hkv * G, Hkv, D, P, 5))
+    assert clean()
+
+
 @pytest.mark.parametrize("D,Hkv,G,P", SHAPES[::3])
 @pytest.mark.parametrize("W", [1, 7, 16, 100, 1024, 5000])
 def test_paged_decode_window(D, Hkv, G, P, W):

@@ -80,9 +80,8 @@ def test_no_tokens_is_no_work(lib):
 def test_workspace_sizes(lib):
     assert lib.g3attn_page_select_workspace_size(64, 16, 2048) == 64 * 16 * 2048 * 4
     assert lib.g3attn_page_select_workspace_size(0, 16, 2048) == 0
-    assert lib.g3attn_paged_decode_workspace_size(1, 96) == 0 and lib.g3attn_paged_decode_workspace_size(8193, 128) == 0
-    # two partial softmaxes per block, whatever the lengths
-    assert lib.g3attn_paged_decode_workspace_size(64, 128) >= 2 * 148 * 8 * 128 * 4
+    # two partial softmaxes per block, whatever the batch and the lengths
+    assert lib.g3attn_paged_decode_workspace_size(96) == 0 and lib.g3attn_paged_decode_workspace_size(128) >= 2 * 148 * 8 * 128 * 4
 
 
 def test_binding_refuses_cpu_tensors():
