@@ -988,6 +988,7 @@ g3_status g3attn_page_bounds(const void* k_pages, const int32_t* block_table, co
 
 size_t g3attn_page_select_workspace_size(int32_t B, int32_t Hkv, int32_t max_pages) {
   if (B < 1 || Hkv < 1 || max_pages < 1) return 0;
+  if (max_pages <= g3::kKeysInSmem) return 256;  // the scores stay on chip
   return align_up((size_t)B * Hkv * max_pages * 4, 256);
 }
 
@@ -1016,7 +1017,7 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
   p.exps = exps;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
-  p.scores = static_cast<float*>(workspace);
+  p.keys = static_cast<uint32_t*>(workspace);
   p.pages = pages;
   p.status = status;
   p.B = B;

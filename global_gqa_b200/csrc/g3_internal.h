@@ -233,16 +233,18 @@ struct PageBoundsParams {
 };
 cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st);
 
+constexpr int kKeysInSmem = 4096;  // page scores that a block keeps in shared memory
 struct PageSelectParams {
   const __nv_bfloat16* q_hat;  // [B, Hq, D]
   const int8_t* bounds;
   const int8_t* exps;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  float* scores;   // [B, Hkv, max_pages]
+  uint32_t* keys;  // [B, Hkv, max_pages] scores as ordered integers, where max_pages > kKeysInSmem
   int32_t* pages;  // [B, Hkv, n_select]
   int* status;
   int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select;
+  int by_length;  // set by the launcher: blocks take the long sequences first
 };
 cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st);
 

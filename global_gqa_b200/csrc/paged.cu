@@ -474,15 +474,18 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
 // numbers below 2^24 in any order, so the scores are exact and the selection does
 // not depend on how they are summed.  HBM-bound: 2D + 1 bytes per (page, kv head).
 //
-// A cluster of blocks takes one (sequence, kv head); the warps of each block bring
-// the group's queries to 8 bits, one head each, then score 16 pages at a time as
-// mma.m16n8k32 of 8-bit whole numbers: rows are pages, columns the group's heads.
-// Each lane loads 16-byte pieces of two pages' bounds straight into its A
-// fragments; the order of the features inside a product is free, so the pieces
-// are used as they come and the query is laid out to match.  Behind the cluster's
-// barrier its first block picks the pages: the scores as ordered integers, the
-// threshold by 8-bit digits below the highest bit in which they differ, then an
-// ordered write.
+// The warps of a block bring the group's queries to 8 bits, one head each, then
+// score 16 pages at a time as mma.m16n8k32 of 8-bit whole numbers: rows are pages,
+// columns the group's heads.  Each lane loads 16-byte pieces of two pages' bounds
+// straight into its A fragments; the order of the features inside a product is
+// free, so the pieces are used as they come and the query is laid out to match.
+// (The same on fp16 numbers made from the bytes took half as long again, dp4a a
+// tenth longer.)
+//
+// A cluster of blocks scores a pair (sequence, kv head) into the shared memory of
+// its first block, which picks behind the cluster's barrier: the scores as ordered
+// integers, the threshold by 8-bit digits below the highest bit in which they
+// differ, then an ordered write.
 constexpr int kSelectThreads = 256;
 constexpr int kSelectWarps = kSelectThreads / 32;
 
@@ -499,19 +502,118 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Pages of a sequence; 0 for a length out of range.
+__device__ __forceinline__ int pages_of(const PageSelectParams& p, int b, bool report) {
+  const int L = p.seq_lens[b];
+  if (L < 0 || L > (long long)p.max_pages << p.page_shift) {
+    if (report) record_error(p.status, kErrInvalid, 330);
+    return 0;
+  }
+  return (L + (1 << p.page_shift) - 1) >> p.page_shift;
+}
+
+// One head of a group in 8 bits, held by the lanes of a warp: loaded, then laid out.
+template <int D>
+struct QueryHead {
+  static constexpr int FPL = D / 32;
+  static constexpr int ROW = 2 * D + 64;  // bytes from one head to the next: 16-byte reads without conflicts
+  float x[FPL];
+  __device__ void load(const PageSelectParams& p, int b, int h, int g, int lane) {
+#pragma unroll
+    for (int i = 0; i < FPL; ++i)
+      x[i] = g < p.G ? __bfloat162float(p.q_hat[((size_t)b * p.Hq + h * p.G + g) * D + i * 32 + lane]) : 0.f;
+  }
+  // Positive parts, then negative parts, to q8's row g; the unit 2^-eq to unit[g].
+  __device__ void store(int8_t* q8, float* unit, int g, int lane) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < FPL; ++i) {
+      if (x[i] != x[i]) x[i] = 0.f;
+      amax = max(amax, (__float_as_uint(x[i]) & 0x7fffffffu) >> 16);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const int e = bound_exponent(amax);
+    const float up = exp2_int(e);
+#pragma unroll
+    for (int i = 0; i < FPL; ++i) {
+      const int v = (int)fminf(fmaxf(rintf(x[i] * up), -127.f), 127.f);
+      q8[g * ROW + i * 32 + lane] = (int8_t)max(v, 0);
+      q8[g * ROW + D + i * 32 + lane] = (int8_t)min(v, 0);
+    }
+    if (lane == 0) unit[g] = exp2_int(-e);
+  }
+};
+
+// Scores pages j0 .. j0 + 15, then every `step`-th such run below `end`, of one pair
+// with np pages, by one warp; put(page, key) receives each once.
+template <int D, class Put>
+__device__ __forceinline__ void score_pages(const PageSelectParams& p, const int32_t* table, int h, int np, int j0, int end, int step,
+                                            const int8_t* q8, const float* unit, Put&& put) {
+  constexpr int PIECES = 2 * D / 64;  // 16-byte pieces of a page's bounds per lane
+  const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
+  const float unit0 = unit[2 * c], unit1 = unit[2 * c + 1];
+  const bool has0 = 2 * c < p.G, has1 = 2 * c + 1 < p.G;
+  int id0 = 0, id1 = 0;
+  if (j0 < end) {
+    id0 = table[min(j0 + row, np - 1)];
+    id1 = table[min(j0 + row + 8, np - 1)];
+  }
+  for (; j0 < end; j0 += step) {
+    // Physical pages of rows `row` and `row + 8` (past the last page it is repeated); a bad one scores -infinity.
+    const bool bad0 = id0 < 0 || id0 >= p.n_pages, bad1 = id1 < 0 || id1 >= p.n_pages;
+    if (bad0 || bad1) record_error(p.status, kErrInvalid, 331);
+    const size_t ph0 = (size_t)(bad0 ? 0 : id0) * p.Hkv + h, ph1 = (size_t)(bad1 ? 0 : id1) * p.Hkv + h;
+    const uint4* s0 = reinterpret_cast<const uint4*>(p.bounds + ph0 * 2 * D) + c;
+    const uint4* s1 = reinterpret_cast<const uint4*>(p.bounds + ph1 * 2 * D) + c;
+    uint4 a0[PIECES], a1[PIECES];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      a0[k] = __ldg(s0 + 4 * k);
+      a1[k] = __ldg(s1 + 4 * k);
+    }
+    const int e0 = p.exps[ph0], e1 = p.exps[ph1];
+    if (j0 + step < end) {
+      id0 = table[min(j0 + step + row, np - 1)];
+      id1 = table[min(j0 + step + row + 8, np - 1)];
+    }
+    int acc[2][4] = {};  // two chains
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const uint4 q = *reinterpret_cast<const uint4*>(&q8[row * QueryHead<D>::ROW + c * 16 + 64 * k]);
+      mma_s8(acc[0], a0[k].x, a1[k].x, a0[k].y, a1[k].y, q.x, q.y);
+      mma_s8(acc[1], a0[k].z, a1[k].z, a0[k].w, a1[k].w, q.z, q.w);
+    }
+    // Page row / row + 8, heads 2c and 2c + 1.
+    const float lo0 = (float)(acc[0][0] + acc[1][0]) * unit0, lo1 = (float)(acc[0][1] + acc[1][1]) * unit1;
+    const float hi0 = (float)(acc[0][2] + acc[1][2]) * unit0, hi1 = (float)(acc[0][3] + acc[1][3]) * unit1;
+    float s_lo = fmaxf(has0 ? lo0 : -INFINITY, has1 ? lo1 : -INFINITY) * exp2_int(-e0);
+    float s_hi = fmaxf(has0 ? hi0 : -INFINITY, has1 ? hi1 : -INFINITY) * exp2_int(-e1);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      s_lo = fmaxf(s_lo, __shfl_xor_sync(0xffffffffu, s_lo, off));
+      s_hi = fmaxf(s_hi, __shfl_xor_sync(0xffffffffu, s_hi, off));
+    }
+    if (c == 0) {
+      if (j0 + row < np) put(j0 + row, ordered_bits(bad0 ? -INFINITY : s_lo));
+      if (j0 + row + 8 < np) put(j0 + row + 8, ordered_bits(bad1 ? -INFINITY : s_hi));
+    }
+  }
+}
+
 struct PickSmem {
+  uint32_t keys[kKeysInSmem];
   uint32_t hist[256];
   uint32_t digit, left, count;
   uint32_t lo[kSelectWarps], hi[kSelectWarps];
   int gt[kSelectWarps], eq[kSelectWarps];
 };
 
-// The k highest of n scores (0 < k < n), equal ones by the lower index, in
-// ascending order of the index, by the whole block.
-__device__ __forceinline__ void pick_pages(const float* sc, int n, int k, int32_t* out, PickSmem& sm) {
+// The k highest of n keys (0 < k < n), equal ones by the lower index, in ascending
+// order of the index, by the whole block.
+template <class Key>
+__device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out, PickSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // Scores come from other blocks: read them where they are written, in L2.
-  auto key = [&](int i) { return ordered_bits(__ldcg(sc + i)); };
   uint32_t lo = 0xffffffffu, hi = 0;
   for (int i = tid; i < n; i += kSelectThreads) {
     const uint32_t u = key(i);
@@ -616,118 +718,83 @@ __device__ __forceinline__ void pick_pages(const float* sc, int n, int k, int32_
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_kernel(PageSelectParams p) {
-  constexpr int PIECES = 2 * D / 64;  // 16-byte pieces of a page's bounds per lane
-  constexpr int FPL = D / 32;         // query features per lane
-  constexpr int QROW = 2 * D + 64;    // bytes from one head's row to the next: 16-byte reads of 8 rows without conflicts
-  __shared__ __align__(16) int8_t q8[8 * QROW];
-  __shared__ float q_unit[8];
-  __shared__ PickSmem pick;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = lane >> 2, c = lane & 3;
-  const int ranks = cluster_size(), rank = blockIdx.x % ranks;
-  const int pair = blockIdx.x / ranks, b = pair / p.Hkv, h = pair % p.Hkv;
-  griddep_wait();
-  griddep_launch();
-  const int L = p.seq_lens[b];
-  // The group's queries are on their way while the length is read.
-  float x[FPL];
-#pragma unroll
-  for (int i = 0; i < FPL; ++i)
-    x[i] = warp < p.G ? __bfloat162float(p.q_hat[((size_t)b * p.Hq + h * p.G + warp) * D + i * 32 + lane]) : 0.f;
-  const bool valid = L >= 0 && L <= (long long)p.max_pages << p.page_shift;
-  if (!valid && rank == 0 && tid == 0) record_error(p.status, kErrInvalid, 330);
-  const int np = valid ? (L + (1 << p.page_shift) - 1) >> p.page_shift : 0;
-  int32_t* out = p.pages + (size_t)pair * p.n_select;
-  if (np <= p.n_select) {  // no choice (the same for the whole cluster)
-    if (rank == 0)
-      for (int i = tid; i < p.n_select; i += kSelectThreads) out[i] = i < np ? i : -1;
-    return;
-  }
-  float* scores = p.scores + (size_t)pair * p.max_pages;
-  {
-    // 8 bits: positive parts, then negative parts.
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < FPL; ++i) {
-      if (x[i] != x[i]) x[i] = 0.f;
-      amax = max(amax, (__float_as_uint(x[i]) & 0x7fffffffu) >> 16);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const int e = bound_exponent(amax);
-    const float unit = exp2_int(e);
-#pragma unroll
-    for (int i = 0; i < FPL; ++i) {
-      const int v = (int)fminf(fmaxf(rintf(x[i] * unit), -127.f), 127.f);
-      q8[warp * QROW + i * 32 + lane] = (int8_t)max(v, 0);
-      q8[warp * QROW + D + i * 32 + lane] = (int8_t)min(v, 0);
-    }
-    if (lane == 0) q_unit[warp] = exp2_int(-e);
-  }
-  __syncthreads();
-  const float unit0 = q_unit[2 * c], unit1 = q_unit[2 * c + 1];
-  const bool has0 = 2 * c < p.G, has1 = 2 * c + 1 < p.G;
-  const int32_t* table = p.block_table + (size_t)b * p.max_pages;
-  const int step = ranks * kSelectWarps * 16;
-  int j0 = (rank * kSelectWarps + warp) * 16;
-  int id0 = 0, id1 = 0;
-  if (j0 < np) {
-    id0 = table[min(j0 + row, np - 1)];
-    id1 = table[min(j0 + row + 8, np - 1)];
-  }
-  for (; j0 < np; j0 += step) {
-    // Physical pages of rows `row` and `row + 8` (past the last page it is repeated); a bad one scores -infinity.
-    const bool bad0 = id0 < 0 || id0 >= p.n_pages, bad1 = id1 < 0 || id1 >= p.n_pages;
-    if (bad0 || bad1) record_error(p.status, kErrInvalid, 331);
-    const size_t ph0 = (size_t)(bad0 ? 0 : id0) * p.Hkv + h, ph1 = (size_t)(bad1 ? 0 : id1) * p.Hkv + h;
-    const uint4* s0 = reinterpret_cast<const uint4*>(p.bounds + ph0 * 2 * D) + c;
-    const uint4* s1 = reinterpret_cast<const uint4*>(p.bounds + ph1 * 2 * D) + c;
-    uint4 a0[PIECES], a1[PIECES];
-#pragma unroll
-    for (int k = 0; k < PIECES; ++k) {
-      a0[k] = __ldg(s0 + 4 * k);
-      a1[k] = __ldg(s1 + 4 * k);
-    }
-    const int e0 = p.exps[ph0], e1 = p.exps[ph1];
-    if (j0 + step < np) {
-      id0 = table[min(j0 + step + row, np - 1)];
-      id1 = table[min(j0 + step + row + 8, np - 1)];
-    }
-    int acc[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < PIECES; ++k) {
-      const uint4 bq = *reinterpret_cast<const uint4*>(&q8[row * QROW + c * 16 + 64 * k]);
-      mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, bq.x, bq.y);
-      mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, bq.z, bq.w);
-    }
-    // acc: page row / row + 8, heads 2c and 2c + 1.
-    float s_lo = fmaxf(has0 ? (float)acc[0] * unit0 : -INFINITY, has1 ? (float)acc[1] * unit1 : -INFINITY) * exp2_int(-e0);
-    float s_hi = fmaxf(has0 ? (float)acc[2] * unit0 : -INFINITY, has1 ? (float)acc[3] * unit1 : -INFINITY) * exp2_int(-e1);
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      s_lo = fmaxf(s_lo, __shfl_xor_sync(0xffffffffu, s_lo, off));
-      s_hi = fmaxf(s_hi, __shfl_xor_sync(0xffffffffu, s_hi, off));
-    }
-    if (c == 0) {
-      if (j0 + row < np) scores[j0 + row] = bad0 ? -INFINITY : s_lo;
-      if (j0 + row + 8 < np) scores[j0 + row + 8] = bad1 ? -INFINITY : s_hi;
-    }
-  }
-  cluster_arrive();  // releases the scores to the cluster
-  if (rank != 0) return;
-  cluster_wait();
-  if (tid == 0) out[p.n_select - 1] = np - 1;
-  if (p.n_select > 1) pick_pages(scores, np - 1, p.n_select - 1, out, pick);
+// The newest page, and the picked ones before it.
+template <class Key>
+__device__ __forceinline__ void write_pages(Key&& key, int np, int n_select, int32_t* out, PickSmem& sm) {
+  if (threadIdx.x == 0) out[n_select - 1] = np - 1;
+  if (n_select > 1) pick_pages(key, np - 1, n_select - 1, out, sm);
+}
+
+// A sequence without a choice: all its pages.
+__device__ __forceinline__ void write_all(int np, int n_select, int32_t* out) {
+  for (int i = threadIdx.x; i < n_select; i += kSelectThreads) out[i] = i < np ? i : -1;
 }
 
 template <int D>
-static cudaError_t launch_select_d(const PageSelectParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_kernel(PageSelectParams p) {
+  __shared__ __align__(16) int8_t q8[8 * QueryHead<D>::ROW];
+  __shared__ float q_unit[8];
+  __shared__ PickSmem pick;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ranks = cluster_size(), rank = blockIdx.x % ranks;
+  const int turn = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
+  int b = turn;
+  cluster_arrive_relaxed();  // waited for before the first store to the first block: it has to be running by then
+  griddep_wait();
+  griddep_launch();
+  if (p.by_length) {
+    // The `turn`-th longest sequence: the blocks that start last have the least to do.
+    __shared__ int s_len[kSelectThreads], s_b;
+    const int t = threadIdx.x, mine = t < p.B ? p.seq_lens[t] : 0;
+    s_len[t] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < p.B; ++j) before += s_len[j] > mine || (s_len[j] == mine && j < t);
+    if (t < p.B && before == turn) s_b = t;
+    __syncthreads();
+    b = s_b;
+  }
+  const int pair = b * p.Hkv + h;
+  QueryHead<D> head;
+  head.load(p, b, h, warp, lane);  // on its way while the length is read
+  const int np = pages_of(p, b, rank == 0 && threadIdx.x == 0);
+  int32_t* out = p.pages + (size_t)pair * p.n_select;
+  if (np <= p.n_select) {  // the same for the whole cluster
+    if (rank == 0) write_all(np, p.n_select, out);
+    return;
+  }
+  head.store(q8, q_unit, warp, lane);
+  __syncthreads();
+  cluster_wait();
+  const int32_t* table = p.block_table + (size_t)b * p.max_pages;
+  uint32_t* keys = p.keys + (size_t)pair * p.max_pages;
+  const bool in_smem = np <= kKeysInSmem;
+  const uint32_t first_keys = cluster_address(pick.keys, 0);
+  score_pages<D>(p, table, h, np, (rank * kSelectWarps + warp) * 16, np, ranks * kSelectWarps * 16, q8, q_unit,
+                 [&](int j, uint32_t key) {
+                   if (in_smem)
+                     cluster_store(first_keys + 4 * j, key);
+                   else
+                     keys[j] = key;
+                 });
+  cluster_arrive();  // releases the keys to the cluster
+  if (rank != 0) return;
+  cluster_wait();
+  if (in_smem)
+    write_pages([&](int i) { return pick.keys[i]; }, np, p.n_select, out, pick);
+  else  // other blocks wrote them: read where they are written, in L2
+    write_pages([&](int i) { return __ldcg(keys + i); }, np, p.n_select, out, pick);
+}
+
+template <int D>
+static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   const long long pairs = (long long)p.B * p.Hkv;
-  // Blocks per pair: up to 8 while they find a place at once, at least 16 pages for each of their warps.
+  // Blocks per pair: up to 8, at least 16 pages for each of their warps, no more than find a place at once.
   int ranks = 1;
-  while (ranks < 8 && (long long)ranks * kSelectWarps * 16 < p.max_pages && pairs * ranks < 148 * 8) ranks *= 2;
+  while (ranks < 8 && ranks * kSelectWarps * 16 < p.max_pages && pairs * ranks < 148 * 2) ranks *= 2;
+  // More blocks than find a place at once: the long sequences first (SELECT_LPT against SELECT_ONE us for 1024 pairs of up to
+  // 2048 pages), as far as a block can rank them with a thread each.
+  p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= kSelectThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
   cfg.blockDim = dim3(kSelectThreads);

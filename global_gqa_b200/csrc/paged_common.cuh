@@ -26,7 +26,18 @@ __device__ __forceinline__ int cluster_size() {
 // The cluster's barrier in two halves: what a thread wrote before its arrival is
 // visible to those that have waited.  A block that only arrives may end.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The address of a shared variable in block `rank` of the cluster, and a store to one.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_store(uint32_t address, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(address), "r"(v) : "memory");
+}
 
 // Inclusive prefix sums of count(b), b < n, into pref[1 .. n], pref[0] = 0, by
 // the whole block (a multiple of 32 threads; `warp_sums` holds one int per

@@ -265,6 +265,36 @@ def test_page_select(D, Hkv, G, P, n):
     assert clean()
 
 
+def test_page_select_longest():
+    """More pages than a block keeps the scores of: ties and a long list."""
+    P, D, n = 16, 64, 1500
+    rng, g = np.random.default_rng(8), torch.Generator().manual_seed(8)
+    lens = [6000 * P, 4096 * P, 4097 * P - 3, 100]
+    table, n_pages = scattered(rng, lens, P)
+    bounds = torch.randint(-9, 10, (n_pages, 1, 2, D), generator=g).to(torch.int8)
+    check_select(torch.randn(4, 2, D, generator=g).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
+    check_select(torch.zeros(4, 2, D).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
+    assert clean()
+
+
+@pytest.mark.parametrize("B", [100, 256, 300])
+def test_page_select_many_sequences(B):
+    """More pairs than find a place at once: taken by length, up to 256 sequences, equal and idle ones among them."""
+    P, D, Hkv, n = 16, 128, 8, 4
+    rng, g = np.random.default_rng(B), torch.Generator().manual_seed(B)
+    lens = rng.integers(0, 30 * P, B)
+    lens[::3] = 25 * P
+    lens[1::5] = 0
+    table, n_pages = scattered(rng, lens, P)
+    bounds = torch.randint(-127, 128, (n_pages, Hkv, 2, D), generator=g).to(torch.int8)
+    check_select(torch.randn(B, Hkv, D, generator=g).bfloat16(), bounds, torch.full((n_pages, Hkv), 4, dtype=torch.int8), table, lens, P, n)
+    assert clean()
+    lens[7], lens[11] = -5, 2 ** 31 - 1
+    got = g3.page_select(torch.randn(B, Hkv, D, generator=g).bfloat16().to(dev()), bounds.to(dev()),
+                         torch.full((n_pages, Hkv), 4, dtype=torch.int8, device=dev()), gi(table), gi(lens), P, n)
+    assert reported() and (got[7] == -1).all() and (got[11] == -1).all() and (got[0, :, -1] == 24).all()
+
+
 def test_page_select_ties_extremes_and_nan():
     P, D, Hkv, n = 16, 64, 2, 9
     rng, g = np.random.default_rng(5), torch.Generator().manual_seed(5)
@@ -278,6 +308,24 @@ def test_page_select_ties_extremes_and_nan():
     q[0, 0, 3], q[1, 2, 7], q[1, 3, 0] = float("nan"), float("inf"), -float("inf")
     exps[::3], exps[1::3] = -50, 50
     check_select(q, bounds, exps, table, lens, P, n)
+    assert clean()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_page_select_largest_sums(D):
+    """Sums of D products of 127 * 127 that differ by one unit in few places are told apart."""
+    P, n = 16, 40
+    rng = np.random.default_rng(D)
+    table, n_pages = scattered(rng, [300 * P], P)
+    for sign in (1, -1):
+        q = sign * torch.full((1, 8, D), 127.0).bfloat16()
+        q[0, 1:, ::2] *= -1
+        bounds = torch.full((n_pages, 1, 2, D), 127, dtype=torch.int8)
+        bounds[:, :, 1] = -127
+        at = torch.from_numpy(rng.integers(0, D, n_pages))
+        bounds[torch.arange(n_pages), 0, 0 if sign == 1 else 1, at] -= sign * torch.from_numpy(rng.integers(0, 3, n_pages)).to(torch.int8)
+        check_select(q, bounds, torch.zeros(n_pages, 1, dtype=torch.int8), table, [300 * P], P, n)
+        check_select(q, -bounds, torch.zeros(n_pages, 1, dtype=torch.int8), table, [300 * P], P, n)
     assert clean()
 
 
