@@ -899,6 +899,7 @@ g3_status g3attn_page_map(const int32_t* old_lens, const int32_t* new_lens, int3
   p.page_shift = page_shift_of(page_size);
   p.n_pages = n_pages;
   p.max_tokens = max_tokens;
+  p.wide = aligned16(slots) && aligned16(positions) ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = traced("page_map", st, [&] { return g3::launch_page_map(p, st); });
   if (e != cudaSuccess) return fail(G3_ERR_CUDA, "page_map: %s", cudaGetErrorString(e));

@@ -105,17 +105,32 @@ PyObject* page_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t P = c.number(a[5]), n_pages = c.number(a[6]), T = c.number(a[7]);
     int32_t* status = c.status(a[8]);
     if (!c.ok || T < 1 || B > INT32_MAX || pages > INT32_MAX || cap > INT32_MAX) Py_RETURN_NONE;
-    const at::Tensor out[5] = {c.empty({B}, kInt), c.empty({B + 1}, kInt), c.empty({T}, kInt), c.empty({T}, kInt), c.empty({2}, kInt)};
+    // One allocation: five tensors that share its storage, each on a 256-byte boundary.
+    const int64_t sizes[5] = {B, B + 1, T, T, 2};
+    int64_t at = 0, begin[5];
+    for (int i = 0; i < 5; ++i) {
+      begin[i] = at;
+      at += (sizes[i] + 63) / 64 * 64;
+    }
+    const at::Tensor all = c.empty({at}, kInt);
+    at::Tensor out[5];
+    for (int i = 0; i < 5; ++i) {
+      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      out[i].unsafeGetTensorImpl()->set_storage_offset(begin[i]);
+      out[i].unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&sizes[i], 1));
+    }
     auto i32 = [](void* p) { return static_cast<int32_t*>(p); };
     auto o32 = [&](int i) { return static_cast<int32_t*>(out[i].data_ptr()); };
     if (g3attn_page_map(i32(po), i32(pn), (int32_t)B, i32(pt), (int32_t)pages, i32(pf), (int32_t)cap, i32(ps), P, n_pages, T,
                         o32(0), o32(1), o32(2), o32(3), o32(4), status, c.stream()) != G3_OK)
       Py_RETURN_NONE;
-    static const char* const names[5] = {"seq_lens", "cu_tokens", "slots", "positions", "free_state"};
+    static PyObject* const names[5] = {PyUnicode_InternFromString("seq_lens"), PyUnicode_InternFromString("cu_tokens"),
+                                       PyUnicode_InternFromString("slots"), PyUnicode_InternFromString("positions"),
+                                       PyUnicode_InternFromString("free_state")};
     PyObject* d = PyDict_New();
     for (int i = 0; d != nullptr && i < 5; ++i) {
       PyObject* t = THPVariable_Wrap(out[i]);
-      if (t == nullptr || PyDict_SetItemString(d, names[i], t) != 0) Py_CLEAR(d);
+      if (t == nullptr || PyDict_SetItem(d, names[i], t) != 0) Py_CLEAR(d);
       Py_XDECREF(t);
     }
     return d;

@@ -199,6 +199,7 @@ struct PageMapParams {
   int32_t* free_state_out;    // [2]
   int* status;                // [2] or null
   int B, max_pages, free_cap, page_size, page_shift, n_pages, max_tokens;
+  int wide;  // slots and positions are 16-byte aligned
 };
 cudaError_t launch_page_map(const PageMapParams& p, cudaStream_t st);
 

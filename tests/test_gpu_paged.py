@@ -80,6 +80,20 @@ def test_page_map(B, P, old_hi, new_hi, spare):
         run_map(*random_map(np.random.default_rng(seed * 1000 + B), B, P, old_hi, new_hi, spare))
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+def test_page_map_long_buffer(offset):
+    """More rows than threads: several per thread, also where the outputs are not aligned."""
+    args = random_map(np.random.default_rng(offset), 600, 16, 100, 900, 3)
+    old, new, table, ring, state, P, n_pages, T = args
+    T = 200001
+    td, ref = gi(table), PG.page_map(old, new, table, ring, state, P, n_pages, T)
+    out = {k: torch.empty(T + 1, dtype=i32, device=dev())[offset:T + offset] for k in ("slots", "positions")}
+    got = g3.page_map(gi(old), gi(new), td, gi(ring), gi(state), P, n_pages, T, out=out)
+    assert (reported() if ref["error"] else clean()) and got["slots"] is out["slots"] and td.cpu().tolist() == ref["table"].tolist()
+    for k in ("seq_lens", "cu_tokens", "slots", "positions", "free_state"):
+        assert got[k].cpu().tolist() == ref[k].tolist(), k
+
+
 def test_page_map_refuses_single_sequences():
     table, ring = np.full((6, 4), -1), np.arange(40)
     table[:, 0] = [30, 31, -1, 33, 99, 35]
