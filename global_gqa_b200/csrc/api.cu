@@ -861,11 +861,11 @@ g3_status g3attn_page_map(const int32_t* old_lens, const int32_t* new_lens, int3
                           int32_t* seq_lens, int32_t* cu_tokens, int32_t* slots, int32_t* positions,
                           int32_t* free_state_out, int32_t* status, void* stream) {
   g_last_error.clear();
+  if (free_capacity < 1 || max_tokens < 1 || max_tokens == 0x7fffffff)
+    return fail(G3_ERR_INVALID_ARG, "page_map: bad free_capacity %d or max_tokens %d", free_capacity, max_tokens);
   if (!old_lens || !new_lens || !block_table || !free_pages || !free_state || !seq_lens || !cu_tokens || !slots ||
       !positions || !free_state_out)
     return fail(G3_ERR_INVALID_ARG, "page_map: a required pointer is NULL");
-  if (free_capacity < 1 || max_tokens < 1 || max_tokens == 0x7fffffff)
-    return fail(G3_ERR_INVALID_ARG, "page_map: bad free_capacity %d or max_tokens %d", free_capacity, max_tokens);
   const g3_status s = check_pool("page_map", B, max_pages, n_pages, page_size, 1, 0);
   if (s != G3_OK) return s;
   // Every block reads all inputs while others write: no output may lie on an input or on another output.
@@ -998,9 +998,9 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
                              int32_t Hq, int32_t Hkv, int32_t D, int32_t n_select, int32_t* pages, void* workspace,
                              size_t workspace_bytes, int32_t* status, void* stream) {
   g_last_error.clear();
+  if (n_select < 1) return fail(G3_ERR_INVALID_ARG, "page_select: n_select=%d", n_select);
   if (!q_hat || !bounds || !exps || !block_table || !seq_lens || !pages)
     return fail(G3_ERR_INVALID_ARG, "page_select: a required pointer is NULL");
-  if (n_select < 1) return fail(G3_ERR_INVALID_ARG, "page_select: n_select=%d", n_select);
   if ((long long)B * Hkv > 0x7fffffffLL / 8) return fail(G3_ERR_UNSUPPORTED, "page_select: %d x %d pairs are too many", B, Hkv);
   g3_status s = check_pool("page_select", B, max_pages, n_pages, page_size, Hkv, D < 1 ? -1 : D);
   if (s == G3_OK) s = check_group("page_select", Hq, Hkv);

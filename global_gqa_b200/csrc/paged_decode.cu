@@ -321,16 +321,22 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 5 : D == 128 ? 3 : 2)
         const float p2 = ex2_approx(s[2] - b0), p3 = ex2_approx(s[3] - b1);
         l0 += p0 + p2;
         l1 += p1 + p3;
-        // P in bf16 for the product with V, as in prefill: at most 2^-8 of each weight, independent over
-        // the tokens, beside the output's own rounding of 2^-8; the sum l keeps fp32.
-        const uint32_t pb0 = transpose8(pack_bf16x2(p0, p1)), pb1 = transpose8(pack_bf16x2(p2, p3));
+        // P as the sum of two bf16 numbers, which leaves 2^-16 of each weight: P V then has fp32's precision up to the
+        // output's rounding.  One bf16 number alone adds an error as large as that rounding, and saves nothing that
+        // can be measured: the second product runs under the loads.
+        const uint32_t ph01 = pack_bf16x2(p0, p1), ph23 = pack_bf16x2(p2, p3);
+        const uint32_t pb0 = transpose8(ph01), pb1 = transpose8(ph23);
+        const uint32_t pl0 = transpose8(pack_bf16x2(p0 - __uint_as_float(ph01 << 16), p1 - __uint_as_float(ph01 & 0xffff0000u)));
+        const uint32_t pl1 = transpose8(pack_bf16x2(p2 - __uint_as_float(ph23 << 16), p3 - __uint_as_float(ph23 & 0xffff0000u)));
 #pragma unroll
         for (int j = 0; j < VP; ++j)
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const uint32_t u0 = piece(vx[0][j], t), u1 = piece(vx[1][j], t), u2 = piece(vx[2][j], t), u3 = piece(vx[3][j], t);
-            mma_bf16(o[j][t], __byte_perm(u0, u1, 0x5410), __byte_perm(u0, u1, 0x7632), __byte_perm(u2, u3, 0x5410),
-                     __byte_perm(u2, u3, 0x7632), pb0, pb1);
+            const uint32_t v0 = __byte_perm(u0, u1, 0x5410), v1 = __byte_perm(u0, u1, 0x7632), v2 = __byte_perm(u2, u3, 0x5410),
+                           v3 = __byte_perm(u2, u3, 0x7632);
+            mma_bf16(o[j][t], v0, v1, v2, v3, pb0, pb1);
+            mma_bf16(o[j][t], v0, v1, v2, v3, pl0, pl1);
           }
       } else {
         load_k(r_next);

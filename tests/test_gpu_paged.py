@@ -5,10 +5,11 @@ of the value.  Whole-number results are equal.
   * q_hat and cached keys: one such rounding of y1 c - y2 s, whose fp32 terms
     are within 2^-18 of |y1| + |y2| (a sum of D squares, a reciprocal root, two
     products: some 30 roundings of 2^-24, 20 of them in the sum of squares).
-  * decode: the output's rounding, 2^-8 |ref|, and P's, 2^-8 of each weight, which
-    moves the output by at most 2^-8 times the weighted mean of |v|; the fp32 sums
+  * decode: the output's rounding, 2^-8 |ref|, and P's, 2^-16 of each weight, which
+    moves the output by at most 2^-16 times the weighted mean of |v|; the fp32 sums
     of q . k, at most (D + 8) 2^-24 of sum |q k| / sqrt D per exponent, move it by
-    twice that share of the same mean.
+    twice that share of the same mean, and those of P V, 2^-24 for each step of 16
+    tokens and some 100 in the merges, by twice as much of it again.
   * lse: that bound on an exponent, and 2^-20 of its own size for the logarithm.
 """
 import numpy as np
@@ -354,11 +355,11 @@ def test_page_select_bad_lengths_and_pages():
 
 
 # ------------------------------------------------------------------ decode
-def near_decode(out, lse, ref, D):
+def near_decode(out, lse, ref, D, longest):
     r, rl, mean_v, s_abs = ref
     got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
     e = ((D + 8) * 2.0 ** -24 * s_abs)[..., None]
-    tol = 2.0 ** -8 * np.abs(r) + (2.0 ** -8 + 2 * e) * (1 + 2.0 ** -7) * mean_v + 1e-30
+    tol = 2.0 ** -8 * np.abs(r) + (2.0 ** -16 + 2 * e + (longest / 8 + 200) * 2.0 ** -24) * (1 + 2.0 ** -7) * mean_v + 1e-30
     assert np.isfinite(got).all()
     assert (np.abs(got - r) <= tol).all(), float((np.abs(got - r) / tol).max())
     assert ((gl == -np.inf) == (rl == -np.inf)).all()
@@ -389,7 +390,7 @@ def run_decode(c, kind=None, W=0, pages=None, **kw):
     out, lse = g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), kind, W,
                                pages=None if pages is None else gi(pages), return_lse=True, **kw)
     ref = PG.paged_decode(c["q"], c["kp"].double().numpy(), c["vp"].double().numpy(), c["table"], c["lens"], kind, W, pages)
-    near_decode(out, lse, ref, c["q"].shape[2])
+    near_decode(out, lse, ref, c["q"].shape[2], int(np.max(c["lens"])))
     return out, lse
 
 
@@ -461,11 +462,9 @@ def test_paged_decode_full_size_sampled():
         idx = torch.as_tensor(table[b, :n], device=dev(), dtype=torch.long)
         ref = PG.paged_decode(q[b:b + 1], kp[idx].double().cpu().numpy(), vp[idx].double().cpu().numpy(), np.arange(n)[None],
                               lens[b:b + 1], 1, 0)
-        near_decode(out[b:b + 1], lse[b:b + 1], ref, D)
+        near_decode(out[b:b + 1], lse[b:b + 1], ref, D, int(lens[b]))
         one = g3.paged_decode(q[b:b + 1].to(dev()), kp, vp, gi(table[b:b + 1]), gi(lens[b:b + 1]), g3.GLOBAL, 0)
-        # cut in other places: each partial rounds P on its own running maximum, so not bit for bit
-        d = (one.float() - out[b:b + 1].float()).abs().cpu().numpy()
-        assert (d <= 2.0 ** -6 * (np.abs(ref[0]) + ref[2])).all()
+        near_decode(one, lse[b:b + 1], ref, D, int(lens[b]))  # cut in other places
     assert clean()
 
 
@@ -509,7 +508,7 @@ def test_paged_decode_bad_pages_lengths_and_lists():
     # [1, 9, 2]: 9 is past the sequence and 2 is not above it; the oracle's list without what is left out
     good[0, 1] = [1, -1, -1]
     ref = PG.paged_decode(c["q"], c["kp"].double().numpy(), c["vp"].double().numpy(), c["table"], lens, 1, 0, good)
-    near_decode(got, torch.from_numpy(ref[1]), ref, 64)
+    near_decode(got, torch.from_numpy(ref[1]), ref, 64, 100)
 
 
 def test_offsets_past_32_bits():
@@ -536,5 +535,5 @@ def test_offsets_past_32_bits():
     out, lse = g3.paged_decode(q_hat[-1:], kp, vp, gi(table), gi([L]), g3.GLOBAL, 0, pages=pages, return_lse=True)
     ref = PG.paged_decode(q_hat[-1:].cpu(), k_small.double().numpy(), v_small.double().numpy(), np.arange(4)[None], [L], 1, 0,
                           pages.cpu().numpy())
-    near_decode(out, lse, ref, D)
+    near_decode(out, lse, ref, D, L)
     assert clean()
