@@ -512,12 +512,12 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
 // columns the group's heads.  Each lane loads 16-byte pieces of two pages' bounds
 // straight into its A fragments; the order of the features inside a product is
 // free, so the pieces are used as they come and the query is laid out to match.
-// (The same on fp16 numbers made from the bytes took half as long again, dp4a a
-// tenth longer.)
+// (The same on fp16 numbers made from the bytes took half as long again, dp4a up
+// to a tenth longer.)
 //
 // A cluster of blocks scores a pair (sequence, kv head) into the shared memory of
 // its first block, which picks behind the cluster's barrier: the scores as ordered
-// integers, the threshold by 8-bit digits below the highest bit in which they
+// integers, the threshold by 11-bit digits below the highest bit in which they
 // differ, then an ordered write.
 constexpr int kSelectThreads = 256;
 constexpr int kSelectWarps = kSelectThreads / 32;
@@ -634,10 +634,11 @@ __device__ __forceinline__ void score_pages(const PageSelectParams& p, const int
   }
 }
 
+constexpr int kPickBits = 11, kPickBins = 1 << kPickBits;
 struct PickSmem {
   uint32_t keys[kKeysInSmem];
-  uint32_t hist[256];
-  uint32_t digit, left, count;
+  __align__(16) uint32_t hist[kPickBins];  // highest digit first
+  uint32_t sums[kSelectWarps], digit, left, count;
   uint32_t lo[kSelectWarps], hi[kSelectWarps];
   int gt[kSelectWarps], eq[kSelectWarps];
 };
@@ -648,20 +649,21 @@ template <class Key>
 __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out, PickSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll 4
   for (int i = tid; i < n; i += kSelectThreads) {
     const uint32_t u = key(i);
     lo = min(lo, u);
     hi = max(hi, u);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
     sm.lo[warp] = lo;
     sm.hi[warp] = hi;
   }
+  // Bins tid * 8 .. tid * 8 + 7 of the histogram belong to this thread.
+  uint4* mine = reinterpret_cast<uint4*>(sm.hist) + 2 * tid;
+  mine[0] = mine[1] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) {
@@ -672,42 +674,42 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
   uint32_t prefix = 0, left = k;
   int shift = 32 - __clz(hi - lo);
   while (shift > 0) {
-    const int next = max(shift - 8, 0), bits = shift - next;
-    sm.hist[tid] = 0;
-    __syncthreads();
+    const int next = max(shift - kPickBits, 0), bits = shift - next;
+#pragma unroll 4
     for (int i = tid; i < n; i += kSelectThreads) {
       const uint32_t u = key(i) - lo;
-      if (shift == 32 || (u >> shift) == prefix) atomicAdd(&sm.hist[(u >> next) & ((1u << bits) - 1u)], 1u);
+      if (shift == 32 || (u >> shift) == prefix) atomicAdd(&sm.hist[kPickBins - 1 - ((u >> next) & ((1u << bits) - 1u))], 1u);
     }
     __syncthreads();
-    if (warp == 0) {
-      // Lane l holds digits 255 - 8l .. 248 - 8l: the digit at which the count from above reaches `left`.
-      uint32_t d[8], sum = 0;
+    const uint4 d0 = mine[0], d1 = mine[1];
+    const uint32_t d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+    const uint32_t sum = d[0] + d[1] + d[2] + d[3] + d[4] + d[5] + d[6] + d[7];
+    uint32_t before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, before, off);
+      if (lane >= off) before += v;
+    }
+    if (lane == 31) sm.sums[warp] = before;
+    mine[0] = mine[1] = make_uint4(0u, 0u, 0u, 0u);  // for a finer digit
+    __syncthreads();
+    before -= sum;
+#pragma unroll
+    for (int w = 0; w < kSelectWarps; ++w) before += w < warp ? sm.sums[w] : 0u;
+    if (before < left && before + sum >= left) {  // one thread: the digit at which the count from above reaches `left`
+      uint32_t digit = 0, count = 0, taken = before;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = sm.hist[255 - (lane * 8 + i)];
-        sum += d[i];
-      }
-      uint32_t inc = sum;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      uint32_t before = inc - sum;
-      if (before < left && inc >= left) {
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!found && before + d[i] >= left) {
-            sm.digit = 255 - (lane * 8 + i);
-            sm.left = left - before;
-            sm.count = d[i];
-            found = true;
-          }
-          before += d[i];
+        if (before < left) {
+          digit = kPickBins - 1 - (tid * 8 + i);
+          count = d[i];
+          taken = before;
         }
+        before += d[i];
       }
+      sm.digit = digit;
+      sm.count = count;
+      sm.left = left - taken;
     }
     __syncthreads();
     prefix = (shift == 32 ? 0u : prefix << bits) | sm.digit;
@@ -717,16 +719,14 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
   }
   const int per = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
   int gt = 0, eq = 0;
+#pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t u = (key(i) - lo) >> shift;
     gt += u > prefix;
     eq += u == prefix;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, off);
-    eq += __shfl_xor_sync(0xffffffffu, eq, off);
-  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     sm.gt[warp] = gt;
     sm.eq[warp] = eq;
@@ -825,7 +825,7 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   // Blocks per pair: up to 8, at least 16 pages for each of their warps, no more than find a place at once.
   int ranks = 1;
   while (ranks < 8 && ranks * kSelectWarps * 16 < p.max_pages && pairs * ranks < 148 * 2) ranks *= 2;
-  // More blocks than find a place at once: the long sequences first (SELECT_LPT against SELECT_ONE us for 1024 pairs of up to
+  // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
   p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= kSelectThreads;
   cudaLaunchConfig_t cfg = {};

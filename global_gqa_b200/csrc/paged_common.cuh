@@ -46,6 +46,18 @@ __device__ __forceinline__ void cluster_store(uint32_t address, uint32_t v) {
 template <class F>
 __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F&& count) {
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  if (n <= 32) {  // every warp for itself, writing the same values: no barrier
+    int inc = lane < n ? count(lane) : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (lane < n) pref[lane + 1] = inc;
+    if (lane == 0) pref[0] = 0;
+    __syncwarp();
+    return;
+  }
   const int per = (n + threads - 1) / threads;  // consecutive entries of each thread
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
   int sum = 0;
