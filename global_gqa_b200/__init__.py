@@ -714,6 +714,8 @@ def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int
     n_select, plist = 0, None
     if pages is not None:
         n_select = _shape(pages, "pages", 3)[2]
+        if n_select == 0:
+            raise ValueError("pages has no entries (None attends to all pages)")
         plist = _arg(pages, "pages", i32, (B, Hkv, n_select), dev)
     if out is None:
         out = _empty(stream, dev, bf16, B, Hq, D)

@@ -844,7 +844,8 @@ static g3_status check_pool(const char* who, int32_t B, int32_t max_pages, int32
     return fail(G3_ERR_UNSUPPORTED, "%s: B=%d sequences, at most %d are built", who, B, g3::kPagedMaxSeqs);
   if ((long long)n_pages * page_size > 0x7fffffffLL)
     return fail(G3_ERR_UNSUPPORTED, "%s: %d pages of %d tokens: slots must fit in 31 bits", who, n_pages, page_size);
-  if ((long long)max_pages * page_size > 0x7fffffffLL || Hkv > 0xffff ||
+  // Room for a length to be rounded up to whole pages.
+  if ((long long)max_pages * page_size > 0x7fffffffLL - 256 || Hkv > 0xffff ||
       (long long)B * Hkv > 0x7fffffffLL / ((long long)max_pages * (page_size / 16)))
     return fail(G3_ERR_UNSUPPORTED, "%s: a block table of %d x %d pages with %d kv heads is too large", who, B, max_pages, Hkv);
   return G3_OK;

@@ -228,7 +228,8 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t kind = c.number(a[5]), window = c.number(a[6]);
     void* pp = list == nullptr ? nullptr : c.ptr(a[7], kInt, {B, Hkv, sel});
     int32_t* status = c.status(a[9]);
-    if (!c.ok || n_pages > INT32_MAX || B > INT32_MAX || pages > INT32_MAX || sel > INT32_MAX) Py_RETURN_NONE;
+    if (!c.ok || n_pages > INT32_MAX || B > INT32_MAX || pages > INT32_MAX || sel > INT32_MAX || (list != nullptr && sel == 0))
+      Py_RETURN_NONE;
     const size_t ws_bytes = g3attn_paged_decode_workspace_size((int32_t)D);
     if (ws_bytes == 0) Py_RETURN_NONE;
     const bool with_lse = a[8] == Py_True;

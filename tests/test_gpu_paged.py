@@ -364,7 +364,7 @@ def near_decode(out, lse, ref, D, longest):
     assert (np.abs(got - r) <= tol).all(), float((np.abs(got - r) / tol).max())
     assert ((gl == -np.inf) == (rl == -np.inf)).all()
     seen = rl > -np.inf
-    assert (np.abs(gl - rl)[seen] <= (e[..., 0] + 2.0 ** -20 * (1 + np.abs(rl)))[seen]).all()
+    assert (np.abs(gl[seen] - rl[seen]) <= e[..., 0][seen] + 2.0 ** -20 * (1 + np.abs(rl[seen]))).all()
     assert (got[~seen] == 0).all()
 
 

@@ -295,6 +295,7 @@ def test_binding_refuses_before_anything_runs():
     refused(g3.paged_decode, dec, g3.G3Error, "bad layer kind", layer_kind=5)
     refused(g3.paged_decode, dec, g3.G3Error, "workspace", ws=torch.empty(64, dtype=torch.uint8, device=dev()))
     refused(g3.paged_decode, dec, g3.G3Error, "page list is for global", pages=gi(np.zeros((5, 2, 3))), layer_kind=g3.LOCAL, window=4)
+    refused(g3.paged_decode, dec, ValueError, "no entries", pages=gi(np.zeros((5, 2, 0))))
     refused(g3.paged_decode, dec, ValueError, "pages must have shape", pages=gi(np.zeros((5, 3, 3))))
     sel = dict(q_hat=q, bounds=p.bounds, exps=p.exps, block_table=p.table, seq_lens=p.lens, page_size=16, n_select=3)
     refused(g3.page_select, sel, g3.G3Error, "n_select", n_select=0)

@@ -34,10 +34,12 @@ def test_bounds_hold_every_key_and_scores_every_product():
         keys = torch.from_numpy(rng.normal(size=(rng.integers(1, 17), 64)) * 2.0 ** rng.integers(-9, 9)).bfloat16().double().numpy()
         bounds, e = PG.page_bounds_of(keys)
         assert (keys <= np.ldexp(bounds[0], -e)).all() and (keys >= np.ldexp(bounds[1], -e)).all()
+        assert (np.ldexp(bounds[0] - 1, -e) < keys.max(0)).all() and (np.ldexp(bounds[1] + 1, -e) > keys.min(0)).all()  # and no wider
         q = np.rint(rng.normal(size=(3, 64)) * 30)   # whole numbers up to 127 are kept by the rounding of q
         q[:, 0] = 127
         score = PG.page_scores(q, bounds[None], [e])[0]
         assert score >= (keys @ q.T).max()
+        assert score == max(PG.page_scores(row[None], bounds[None], [e])[0] for row in q)
 
 
 def test_pick_ties_and_short_sequences():

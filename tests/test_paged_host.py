@@ -44,6 +44,7 @@ REFUSED = [
     ("page_map", dict(B=8192, max_pages=1 << 18), 2), ("page_map", dict(lens=at(0)), 1),      # in place over an input
     ("page_map", dict(state_out=at(4) + 4), 1), ("page_map", dict(slots=at(8) - 100), 1),     # half over another output
     ("page_map", dict(table=at(3) - 4), 1),
+    ("page_map", dict(B=1, max_pages=(1 << 27) - 1), 2), ("page_bounds", dict(B=1, P=256, max_pages=(1 << 23) - 1), 2),
     ("paged_append", dict(k=None), 1), ("paged_append", dict(T=-1), 1), ("paged_append", dict(base=0.0), 1),
     ("paged_append", dict(base=float("nan")), 1), ("paged_append", dict(interp=float("inf")), 1),
     ("paged_append", dict(Hq=0), 1), ("paged_append", dict(q=None), 1), ("paged_append", dict(qh=None), 1),
