@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   extern __shared__ int map_smem[];
   uint32_t* ends = reinterpret_cast<uint32_t*>(map_smem);  // [B] rows up to and with request b (stops at max_tokens + 1)
   int* cum = map_smem + p.B;                               // [B] pages asked for up to and with request b
+  int* olds = cum + p.B;                                   // [B] tokens cached before, -1 where request b is refused
   __shared__ uint32_t s_rows[32];
   __shared__ int s_need[32];
   __shared__ int s_taken;
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
       ends[b] = rows;
       cum[b] = c;
       const bool granted = valid && (need == 0 || c <= count);
+      olds[b] = granted ? old_len : -1;
       if (granted && need > 0) atomicMax(&s_taken, c);
       if (blockIdx.x == 0) {
         p.seq_lens[b] = granted ? old_len + new_len : (old_len >= 0 && old_len <= room ? old_len : 0);
@@ -124,8 +126,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   // New table entries: one warp per request.
   for (int b = blockIdx.x * (kMapThreads / 32) + warp; b < p.B; b += gridDim.x * (kMapThreads / 32)) {
     const int asked = b > 0 ? cum[b - 1] : 0, need = cum[b] - asked;
-    if (need == 0 || cum[b] > count) continue;
-    const int have = (p.old_lens[b] + p.page_size - 1) >> p.page_shift;
+    if (need == 0 || olds[b] < 0) continue;
+    const int have = (olds[b] + p.page_size - 1) >> p.page_shift;
     for (int i = lane; i < need; i += 32) {
       const int id = fresh_page(asked, i);
       p.block_table[(size_t)b * p.max_pages + have + i] = id;
@@ -151,26 +153,17 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
         else
           hi = mid;
       }
-      int b = hi, known = -1, old_len = 0, asked = 0, begin = 0;
-      bool granted = false;
+      int b = hi;
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) {
         const int t = t0 + k;
         if (t >= p.max_tokens || (uint32_t)t >= rows_end) break;
         while (ends[b] <= (uint32_t)t) ++b;
-        if (b != known) {
-          known = b;
-          old_len = p.old_lens[b];
-          const int new_len = p.new_lens[b];
-          asked = b > 0 ? cum[b - 1] : 0;
-          begin = b > 0 ? (int)ends[b - 1] : 0;
-          granted = old_len >= 0 && new_len >= 0 && (long long)old_len + new_len <= room && ends[b] < cap &&
-                    (cum[b] == asked || cum[b] <= count);
-        }
-        if (!granted) continue;
-        pos[k] = old_len + t - begin;
+        const int old_len = olds[b];
+        if (old_len < 0) continue;
+        pos[k] = old_len + t - (b > 0 ? (int)ends[b - 1] : 0);
         const int j = pos[k] >> p.page_shift, have = (old_len + p.page_size - 1) >> p.page_shift;
-        const int page = j < have ? p.block_table[(size_t)b * p.max_pages + j] : fresh_page(asked, j - have);
+        const int page = j < have ? p.block_table[(size_t)b * p.max_pages + j] : fresh_page(b > 0 ? cum[b - 1] : 0, j - have);
         if (page >= 0 && page < p.n_pages)
           slot[k] = (page << p.page_shift) + (pos[k] & (p.page_size - 1));
         else if (j < have)
@@ -194,10 +187,10 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
 template <int ROWS>
 static cudaError_t launch_map(const PageMapParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = ensure_dynamic_smem(page_map_kernel<ROWS>, 2 * kPagedMaxSeqs * (int)sizeof(int), done);
+  const cudaError_t e = ensure_dynamic_smem(page_map_kernel<ROWS>, 3 * kPagedMaxSeqs * (int)sizeof(int), done);
   if (e != cudaSuccess) return e;
   const int blocks = std::min(p.max_tokens / (kMapThreads * ROWS) + 1, 148);
-  return launch_dependent(page_map_kernel<ROWS>, dim3(blocks), dim3(kMapThreads), 2 * p.B * sizeof(int), st, p);
+  return launch_dependent(page_map_kernel<ROWS>, dim3(blocks), dim3(kMapThreads), 3 * p.B * sizeof(int), st, p);
 }
 
 // One row per thread keeps a step of single tokens short (64 requests: 4.0 us, 5.6 with four: their look-ups follow one
