@@ -525,6 +525,13 @@ def _shape(t, name, n: int):
     return shape
 
 
+def _int32(v, name) -> int:
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:  # ctypes would drop the upper bits
+        raise ValueError(f"{name}={v} does not fit in 32 bits")
+    return v
+
+
 def _gpu_of(t, name):
     dev = t.device
     if dev.type != "cuda":
@@ -584,6 +591,7 @@ def page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size:
         if r is not None:
             return r
     i32 = _torch().int32
+    _int32(max_tokens, "max_tokens")
     B, = _shape(old_lens, "old_lens", 1)
     max_pages = _shape(block_table, "block_table", 2)[1]
     cap, = _shape(free_pages, "free_pages", 1)
@@ -597,7 +605,8 @@ def page_map(old_lens, new_lens, block_table, free_pages, free_state, page_size:
                 _arg(new_lens, "new_lens", i32, (B,), dev), B,
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), max_pages,
                 _arg(free_pages, "free_pages", i32, (cap,), dev), cap, _arg(free_state, "free_state", i32, (2,), dev),
-                page_size, n_pages, max_tokens, _arg(r["seq_lens"], "seq_lens", i32, (B,), dev),
+                _int32(page_size, "page_size"), _int32(n_pages, "n_pages"), max_tokens,
+                _arg(r["seq_lens"], "seq_lens", i32, (B,), dev),
                 _arg(r["cu_tokens"], "cu_tokens", i32, (B + 1,), dev), _arg(r["slots"], "slots", i32, (max_tokens,), dev),
                 _arg(r["positions"], "positions", i32, (max_tokens,), dev),
                 _arg(r["free_state"], "out free_state", i32, (2,), dev))
@@ -678,14 +687,14 @@ def page_select(q_hat, bounds, exps, block_table, seq_lens, page_size: int, n_se
     max_pages = _shape(block_table, "block_table", 2)[1]
     dev = _gpu_of(q_hat, "q_hat")
     if out is None:
-        out = _empty(stream, dev, i32, B, Hkv, max(n_select, 0))
+        out = _empty(stream, dev, i32, B, Hkv, max(_int32(n_select, "n_select"), 0))
     if ws is None:
         ws = _empty(stream, dev, torch.uint8, max(page_select_workspace_size(B, Hkv, max_pages), 1))
     ws, ws_bytes = _ws(ws, 0, dev)
     _paged_call("g3attn_page_select", dev, stream, status, _arg(q_hat, "q_hat", torch.bfloat16, (B, Hq, D), dev),
                 _arg(bounds, "bounds", i8, (n_pages, Hkv, 2, D), dev), _arg(exps, "exps", i8, (n_pages, Hkv), dev),
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), B,
-                max_pages, n_pages, page_size, Hq, Hkv, D, n_select, _arg(out, "out", i32, (B, Hkv, n_select), dev),
+                max_pages, n_pages, _int32(page_size, "page_size"), Hq, Hkv, D, n_select, _arg(out, "out", i32, (B, Hkv, n_select), dev),
                 ws.data_ptr(), ws_bytes)
     return out
 
@@ -726,6 +735,6 @@ def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int
     _paged_call("g3attn_paged_decode", dev, stream, status, _arg(q_hat, "q_hat", bf16, (B, Hq, D), dev),
                 _arg(k_pages, "k_pages", bf16, pool, dev), _arg(v_pages, "v_pages", bf16, pool, dev),
                 _arg(block_table, "block_table", i32, (B, max_pages), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev), plist,
-                n_select, int(layer_kind), int(window), B, max_pages, n_pages, P, Hq, Hkv, D,
+                n_select, _int32(layer_kind, "layer_kind"), _int32(window, "window"), B, max_pages, n_pages, P, Hq, Hkv, D,
                 _arg(out, "out", bf16, (B, Hq, D), dev), _ptr(lse), ws.data_ptr(), ws_bytes)
     return (out, lse) if return_lse else out

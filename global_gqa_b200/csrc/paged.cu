@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
   const int d1 = li * 8;
   const int heads = p.Hq + p.Hkv;  // Hq = 0 without queries
   for (int i = threadIdx.x; i < H2; i += kAppendThreads) inv_freq_s[i] = p.inv_freq[i];
-  griddep_wait();
+  const uint32_t token = griddep_wait_token();
   griddep_launch();
   for (int i = threadIdx.x; i < 2 * D; i += kAppendThreads)
     gam[i] = i >= D ? p.k_gamma[i - D] : p.Hq > 0 ? p.q_gamma[i] : 0.f;
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
         xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
         if (h < heads && (h < p.Hq || keep)) {
           const __nv_bfloat16* src = h < p.Hq ? qrow + h * D : krow + (h - p.Hq) * D;
-          xa[u] = __ldg(reinterpret_cast<const uint4*>(src + d1));
-          xb[u] = __ldg(reinterpret_cast<const uint4*>(src + H2 + d1));
+          xa[u] = ldg_after(src + d1, token);
+          xb[u] = ldg_after(src + H2 + d1, token);
         }
       }
 #pragma unroll
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
           *reinterpret_cast<uint4*>(p.k_pages + at + d1) = pack8(o);
           *reinterpret_cast<uint4*>(p.k_pages + at + H2 + d1) = pack8(o + 8);
           const __nv_bfloat16* vsrc = p.v + ((size_t)t * p.Hkv + kh) * D;
-          *reinterpret_cast<uint4*>(p.v_pages + at + d1) = __ldg(reinterpret_cast<const uint4*>(vsrc + d1));
-          *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = __ldg(reinterpret_cast<const uint4*>(vsrc + H2 + d1));
+          *reinterpret_cast<uint4*>(p.v_pages + at + d1) = ldg_after(vsrc + d1, token);
+          *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = ldg_after(vsrc + H2 + d1, token);
         }
       }
     }

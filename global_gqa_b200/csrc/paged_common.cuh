@@ -39,10 +39,30 @@ __device__ __forceinline__ void cluster_store(uint32_t address, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(address), "r"(v) : "memory");
 }
 
+// griddep_wait(), with a token for reads that must not be moved in front of it.
+__device__ __forceinline__ uint32_t griddep_wait_token() {
+  uint32_t token;
+  asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(token)::"memory");
+  return token;
+}
+// A 16-byte read of data that no one writes during the kernel: free to move, but not before the wait that gave the
+// token (a compiler may take __ldg's address to be readable from the kernel's start).
+__device__ __forceinline__ uint4 ldg_after(const void* p, uint32_t token) {
+  uint4 v;
+  asm("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "r"(token));
+  return v;
+}
+// The same of data that the block reads once, in the order of the program.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // Inclusive prefix sums of count(b), b < n, into pref[1 .. n], pref[0] = 0, by
 // the whole block (a multiple of 32 threads; `warp_sums` holds one int per
-// warp).  Every block of a grid repeats it: a few microseconds at the largest n,
-// for one launch less and no order between blocks.
+// warp).  Every block of a grid repeats it: some microseconds at the largest n, for
+// one launch less and no order between blocks.
 template <class F>
 __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F&& count) {
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
@@ -58,11 +78,16 @@ __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F
     __syncwarp();
     return;
   }
-  const int per = (n + threads - 1) / threads;  // consecutive entries of each thread
+  // The terms first, in coalesced reads that do not wait for one another; then each thread sums a run of its own (of odd
+  // length: the threads' runs begin in different banks).  8192 sequences: 12 us, 90 with the reads in the runs.
+#pragma unroll 8
+  for (int i = tid; i < n; i += threads) pref[i + 1] = count(i);
+  __syncthreads();
+  const int per = ((n + threads - 1) / threads) | 1;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
-    sum += count(i);
+    sum += pref[i + 1];
     pref[i + 1] = sum;
   }
   int inc = sum;

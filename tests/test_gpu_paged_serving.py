@@ -293,6 +293,7 @@ def test_binding_refuses_before_anything_runs():
     refused(g3.paged_decode, dec, ValueError, "out must", out=q[:2])
     refused(g3.paged_decode, dec, g3.G3Error, "window", layer_kind=g3.LOCAL)
     refused(g3.paged_decode, dec, g3.G3Error, "bad layer kind", layer_kind=5)
+    refused(g3.paged_decode, dec, ValueError, "32 bits", layer_kind=g3.LOCAL, window=2 ** 32 + 5)
     refused(g3.paged_decode, dec, g3.G3Error, "workspace", ws=torch.empty(64, dtype=torch.uint8, device=dev()))
     refused(g3.paged_decode, dec, g3.G3Error, "page list is for global", pages=gi(np.zeros((5, 2, 3))), layer_kind=g3.LOCAL, window=4)
     refused(g3.paged_decode, dec, ValueError, "no entries", pages=gi(np.zeros((5, 2, 0))))
@@ -300,6 +301,8 @@ def test_binding_refuses_before_anything_runs():
     sel = dict(q_hat=q, bounds=p.bounds, exps=p.exps, block_table=p.table, seq_lens=p.lens, page_size=16, n_select=3)
     refused(g3.page_select, sel, g3.G3Error, "n_select", n_select=0)
     refused(g3.page_select, sel, g3.G3Error, "page_size", page_size=20)
+    refused(g3.page_select, sel, ValueError, "32 bits", n_select=2 ** 32 + 3)
+    refused(g3.page_select, sel, ValueError, "32 bits", page_size=2 ** 32 + 16)
     refused(g3.page_select, sel, TypeError, "bounds must be", bounds=p.bounds.to(torch.uint8))
     app = dict(k=s.k, v=s.v, k_gamma=s.gain, positions=s.one, slots=s.one, k_pages=p.k[0], v_pages=p.v[0], rope_base=1e4, interp_factor=1.0)
     refused(g3.paged_append, app, ValueError, "q_gamma and q_hat", q_gamma=s.gain)
@@ -310,6 +313,8 @@ def test_binding_refuses_before_anything_runs():
               max_tokens=5)
     refused(g3.page_map, mp, g3.G3Error, "overlaps", out=dict(seq_lens=p.lens))
     refused(g3.page_map, mp, g3.G3Error, "max_tokens", max_tokens=0)
+    refused(g3.page_map, mp, ValueError, "32 bits", max_tokens=2 ** 32 + 5)
+    refused(g3.page_map, mp, ValueError, "32 bits", n_pages=2 ** 32 + 5)
     refused(g3.page_map, mp, ValueError, "free_state must have shape", free_state=p.lens)
     bd = dict(k_pages=p.k[0], block_table=p.table, old_lens=p.lens, seq_lens=p.lens, bounds=p.bounds, exps=p.exps)
     refused(g3.page_bounds, bd, ValueError, "exps must have shape", exps=p.exps[:, :1].contiguous())
