@@ -35,8 +35,8 @@ constexpr int kMapThreads = 1024;
 // enough for any lengths (cap < 2^31).
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap) { return min(a + b, cap); }
 
-template <int ROWS>
-__global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) {
+template <int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
   extern __shared__ int map_smem[];
   uint32_t* ends = reinterpret_cast<uint32_t*>(map_smem);  // [B] rows up to and with request b (stops at max_tokens + 1)
   int* cum = map_smem + p.B;                               // [B] pages asked for up to and with request b
@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   __shared__ uint32_t s_rows[32];
   __shared__ int s_need[32];
   __shared__ int s_taken;
-  griddep_wait();
-  griddep_launch();
+  griddep_wait();  // and its dependents wait for its end: blocks beside these cost 2 of 9 us at 512000 rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int threads = THREADS, warps = THREADS / 32;
   const uint32_t cap = (uint32_t)p.max_tokens + 1u;
   const long long room = (long long)p.max_pages * p.page_size;
   int head = p.free_state[0], count = p.free_state[1];
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   // Rows first: whether a request fits the token buffer decides whether it asks for pages.
   uint32_t rows_before = 0;
   int need_before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kMapThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + tid;
     int old_len = 0, new_len = 0;
     if (b < p.B) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
     uint32_t add = rows_before;
     for (int w = 0; w < warp; ++w) add = sat_add(add, s_rows[w], cap);
     rows = sat_add(rows, add, cap);
-    for (int w = 0; w < kMapThreads / 32; ++w) rows_before = sat_add(rows_before, s_rows[w], cap);
+    for (int w = 0; w < warps; ++w) rows_before = sat_add(rows_before, s_rows[w], cap);
 
     const bool valid = b < p.B && old_len >= 0 && new_len >= 0 && (long long)old_len + new_len <= room && rows < cap;
     const int have = valid ? (old_len + p.page_size - 1) >> p.page_shift : 0;
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
     __syncthreads();
     c += need_before;
     for (int w = 0; w < warp; ++w) c += s_need[w];
-    for (int w = 0; w < kMapThreads / 32; ++w) need_before += s_need[w];
+    for (int w = 0; w < warps; ++w) need_before += s_need[w];
     if (b < p.B) {
       ends[b] = rows;
       cum[b] = c;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   };
 
   // New table entries: one warp per request.
-  for (int b = blockIdx.x * (kMapThreads / 32) + warp; b < p.B; b += gridDim.x * (kMapThreads / 32)) {
+  for (int b = blockIdx.x * (warps) + warp; b < p.B; b += gridDim.x * (warps)) {
     const int asked = b > 0 ? cum[b - 1] : 0, need = cum[b] - asked;
     if (need == 0 || olds[b] < 0) continue;
     const int have = (olds[b] + p.page_size - 1) >> p.page_shift;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
 
   // Slot and position of every row of the token buffer: ROWS of them per thread and search.
   const uint32_t rows_end = ends[p.B - 1];
-  for (int t0 = (blockIdx.x * kMapThreads + tid) * ROWS; t0 < p.max_tokens; t0 += gridDim.x * kMapThreads * ROWS) {
+  for (int t0 = (blockIdx.x * threads + tid) * ROWS; t0 < p.max_tokens; t0 += gridDim.x * threads * ROWS) {
     int slot[ROWS], pos[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
         else
           hi = mid;
       }
-      int b = hi;
+      int b = hi, last_b = -1, last_j = -1, page = -1;
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) {
         const int t = t0 + k;
@@ -162,12 +162,18 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
         const int old_len = olds[b];
         if (old_len < 0) continue;
         pos[k] = old_len + t - (b > 0 ? (int)ends[b - 1] : 0);
-        const int j = pos[k] >> p.page_shift, have = (old_len + p.page_size - 1) >> p.page_shift;
-        const int page = j < have ? p.block_table[(size_t)b * p.max_pages + j] : fresh_page(b > 0 ? cum[b - 1] : 0, j - have);
-        if (page >= 0 && page < p.n_pages)
-          slot[k] = (page << p.page_shift) + (pos[k] & (p.page_size - 1));
-        else if (j < have)
-          record_error(p.status, kErrInvalid, 302);
+        const int j = pos[k] >> p.page_shift;
+        if (b != last_b || j != last_j) {  // rows of one page follow one another: one look-up
+          last_b = b;
+          last_j = j;
+          const int have = (old_len + p.page_size - 1) >> p.page_shift;
+          page = j < have ? p.block_table[(size_t)b * p.max_pages + j] : fresh_page(b > 0 ? cum[b - 1] : 0, j - have);
+          if (page < 0 || page >= p.n_pages) {
+            if (j < have) record_error(p.status, kErrInvalid, 302);
+            page = -1;
+          }
+        }
+        if (page >= 0) slot[k] = (page << p.page_shift) + (pos[k] & (p.page_size - 1));
       }
     }
     if (ROWS == 4 && p.wide && t0 + 4 <= p.max_tokens) {
@@ -184,19 +190,21 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(PageMapParams p) 
   }
 }
 
-template <int ROWS>
+template <int ROWS, int THREADS>
 static cudaError_t launch_map(const PageMapParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = ensure_dynamic_smem(page_map_kernel<ROWS>, 3 * kPagedMaxSeqs * (int)sizeof(int), done);
+  const cudaError_t e = ensure_dynamic_smem(page_map_kernel<ROWS, THREADS>, 3 * kPagedMaxSeqs * (int)sizeof(int), done);
   if (e != cudaSuccess) return e;
-  const int blocks = std::min(p.max_tokens / (kMapThreads * ROWS) + 1, 148);
-  return launch_dependent(page_map_kernel<ROWS>, dim3(blocks), dim3(kMapThreads), 3 * p.B * sizeof(int), st, p);
+  const int blocks = std::min(p.max_tokens / (THREADS * ROWS) + 1, 148 * kMapThreads / THREADS);
+  return launch_dependent(page_map_kernel<ROWS, THREADS>, dim3(blocks), dim3(THREADS), 3 * p.B * sizeof(int), st, p);
 }
 
-// One row per thread keeps a step of single tokens short (64 requests: 4.0 us, 5.6 with four: their look-ups follow one
+// One row per thread keeps a step of single tokens short (64 requests: 4.0 us, 5.6 with four: their look-ups followed one
 // another); four spare most searches and stores where one pass of the grid does not do (512000 rows: 6.5 against 7.7).
+// Half the threads where one pass over the requests takes no more (64 requests: 3.3 us).
 cudaError_t launch_page_map(const PageMapParams& p, cudaStream_t st) {
-  return p.max_tokens <= 148 * kMapThreads ? launch_map<1>(p, st) : launch_map<4>(p, st);
+  if (p.max_tokens > 148 * kMapThreads) return launch_map<4, kMapThreads>(p, st);
+  return p.B <= kMapThreads / 2 ? launch_map<1, kMapThreads / 2>(p, st) : launch_map<1, kMapThreads>(p, st);
 }
 
 // ============================================================= paged append
