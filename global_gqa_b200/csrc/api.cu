@@ -844,9 +844,9 @@ static g3_status check_pool(const char* who, int32_t B, int32_t max_pages, int32
     return fail(G3_ERR_UNSUPPORTED, "%s: B=%d sequences, at most %d are built", who, B, g3::kPagedMaxSeqs);
   if ((long long)n_pages * page_size > 0x7fffffffLL)
     return fail(G3_ERR_UNSUPPORTED, "%s: %d pages of %d tokens: slots must fit in 31 bits", who, n_pages, page_size);
-  // Room for a length to be rounded up to whole pages.
+  // Room for a length to be rounded up to whole pages, and for counts of 16-token units (and a grid's stride) in 32 bits.
   if ((long long)max_pages * page_size > 0x7fffffffLL - 256 || Hkv > 0xffff ||
-      (long long)B * Hkv > 0x7fffffffLL / ((long long)max_pages * (page_size / 16)))
+      (long long)B * Hkv > 0x3fffffffLL / ((long long)max_pages * (page_size / 16)))
     return fail(G3_ERR_UNSUPPORTED, "%s: a block table of %d x %d pages with %d kv heads is too large", who, B, max_pages, Hkv);
   return G3_OK;
 }
@@ -862,8 +862,9 @@ g3_status g3attn_page_map(const int32_t* old_lens, const int32_t* new_lens, int3
                           int32_t* seq_lens, int32_t* cu_tokens, int32_t* slots, int32_t* positions,
                           int32_t* free_state_out, int32_t* status, void* stream) {
   g_last_error.clear();
-  if (free_capacity < 1 || max_tokens < 1 || max_tokens == 0x7fffffff)
+  if (free_capacity < 1 || max_tokens < 1)
     return fail(G3_ERR_INVALID_ARG, "page_map: bad free_capacity %d or max_tokens %d", free_capacity, max_tokens);
+  if (max_tokens > 1 << 30) return fail(G3_ERR_UNSUPPORTED, "page_map: max_tokens %d, at most 2^30 are built", max_tokens);
   if (!old_lens || !new_lens || !block_table || !free_pages || !free_state || !seq_lens || !cu_tokens || !slots ||
       !positions || !free_state_out)
     return fail(G3_ERR_INVALID_ARG, "page_map: a required pointer is NULL");

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
   };
 
   // New table entries: one warp per request.
-  for (int b = blockIdx.x * (warps) + warp; b < p.B; b += gridDim.x * (warps)) {
+  for (int b = blockIdx.x * warps + warp; b < p.B; b += gridDim.x * warps) {
     const int asked = b > 0 ? cum[b - 1] : 0, need = cum[b] - asked;
     if (need == 0 || olds[b] < 0) continue;
     const int have = (olds[b] + p.page_size - 1) >> p.page_shift;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
     }
     return max(0, ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift));
   });
-  const int units = bounds_smem[p.B] * p.Hkv;  // below 2^31: checked on the host for the widest table
+  const int units = bounds_smem[p.B] * p.Hkv;  // below 2^30: checked on the host for the widest table
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LPT, sub = lane / LPT;
   const int P = 1 << p.page_shift;
   constexpr int WARPS = kBoundsThreads / 32;

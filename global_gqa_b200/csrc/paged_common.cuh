@@ -105,7 +105,7 @@ __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F
   __syncthreads();
 }
 
-// The b with pref[b] * scale <= x < pref[b + 1] * scale; 0 <= x < pref[n] * scale < 2^31.
+// The b with pref[b] * scale <= x < pref[b + 1] * scale; 0 <= x < pref[n] * scale < 2^30.
 __device__ __forceinline__ int find_row(const int* pref, int n, int x, int scale) {
   int lo = 0, hi = n;  // pref[lo] * scale <= x < pref[hi] * scale
   while (hi - lo > 1) {

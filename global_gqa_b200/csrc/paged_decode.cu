@@ -69,7 +69,7 @@ __device__ __forceinline__ int units_of(const PagedDecodeParams& p, int b, bool 
   const int lo = p.kind == 0 ? max(0, L - p.window) : 0;
   return (L + kUnit - 1) / kUnit - lo / kUnit;
 }
-// The line of `total` < 2^31 units cut into shares of q or q + 1 for `blocks`
+// The line of `total` < 2^30 units cut into shares of q or q + 1 for `blocks`
 // blocks: none with less than one unit per warp.
 struct Shares {
   int blocks, q, r;  // the first r shares have q + 1 units
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
       store_row<D>(p, (size_t)b * p.Hq + i / (D / 4), i % (D / 4) * 4, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
     for (int h = threadIdx.x; p.deal && h < p.Hkv; h += kPagedThreads) p.cuts[b * p.Hkv + h] = make_int4(-1, 0, 0, 0);
   }
-  const int total = pref[p.B] * p.Hkv;  // below 2^31: checked on the host for the widest table
+  const int total = pref[p.B] * p.Hkv;  // below 2^30: checked on the host for the widest table
   const Shares sh(total, gridDim.x);
   int range0 = 0, range1 = 0, dealt = 1, part = 0;  // units of this block; of its pair, where blocks are dealt
   int* deal = pref + p.B + 1;

@@ -304,7 +304,8 @@ g3_status g3attn_decode_no_alloc(const void* q, const void* k_new, const void* v
  *              values is recorded there and stays until
  *              g3attn_check_device_error(status, stream) reports and clears
  *              it; any number of calls may share it.  NULL: not recorded.
- *   At most 8192 sequences, and 8 query heads per kv head, in one call.
+ *   At most 8192 sequences, 8 query heads per kv head, and tables with
+ *   B * Hkv * max_pages * page_size / 16 < 2^30 in one call.
  * The calls are ordered by their stream alone and may be captured in a graph.
  * A serving step is: page_map once for all layers, then per layer paged_append,
  * (page_bounds and page_select on a sparse global layer,) paged_decode.
@@ -321,7 +322,7 @@ g3_status g3attn_decode_no_alloc(const void* q, const void* k_new, const void* v
  *   free_state int32 [2] = {head, count}: pages are taken from the head on, in
  *              the order of the sequences.  To give pages back, write them
  *              behind the last one ((head + count) % free_capacity) and raise count
- *   max_tokens rows of slots and positions
+ *   max_tokens rows of slots and positions, at most 2^30
  *   seq_lens   int32 [B]  old + new, or old where the sequence was refused
  *   cu_tokens  int32 [B + 1]  first row of each sequence's new tokens in the
  *              packed order of the sequences (refused ones keep their rows)

@@ -41,7 +41,8 @@ REFUSED = [
     ("page_map", dict(old=None), 1), ("page_map", dict(state_out=None), 1), ("page_map", dict(B=0), 1),
     ("page_map", dict(T=0), 1), ("page_map", dict(cap=0), 1), ("page_map", dict(n_pages=0), 1), ("page_map", dict(P=24), 2),
     ("page_map", dict(P=512), 2), ("page_map", dict(B=8193), 2), ("page_map", dict(n_pages=1 << 28), 2),
-    ("page_map", dict(B=8192, max_pages=1 << 18), 2), ("page_map", dict(lens=at(0)), 1),      # in place over an input
+    ("page_map", dict(B=8192, max_pages=1 << 18), 2), ("page_map", dict(T=(1 << 30) + 1), 2),
+    ("page_bounds", dict(B=64, Hkv=16, max_pages=1 << 18), 2), ("paged_decode", dict(B=64, Hq=16, Hkv=16, max_pages=1 << 18), 2), ("page_map", dict(lens=at(0)), 1),      # in place over an input
     ("page_map", dict(state_out=at(4) + 4), 1), ("page_map", dict(slots=at(8) - 100), 1),     # half over another output
     ("page_map", dict(table=at(3) - 4), 1),
     ("page_map", dict(B=1, max_pages=(1 << 27) - 1), 2), ("page_bounds", dict(B=1, P=256, max_pages=(1 << 23) - 1), 2),
