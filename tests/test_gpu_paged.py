@@ -233,6 +233,32 @@ def test_page_bounds(D, Hkv, P):
     assert clean()
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 32), (128, 16)])
+def test_page_bounds_many_small_pages(D, P):
+    """More (page, kv head) pairs than one turn of the grid takes, some pages of them bad: 5 pairs a page, so that a
+    warp's rows belong to different pages."""
+    Hkv, n = 5, 4200
+    rng = np.random.default_rng(D * P)
+    k = torch.randn(n, Hkv, P, D, generator=torch.Generator().manual_seed(P)).bfloat16()
+    lens, old = [n // 2 * P, n // 2 * P - P + 3], [0, P // 2]
+    table = rng.permutation(n).reshape(2, n // 2)
+    bad = [(0, 0), (0, 1), (0, 777), (1, 2), (1, n // 2 - 1)]
+    for i, (b, j) in enumerate(bad):
+        table[b, j] = [n, -1][i % 2]
+    bounds, exps = torch.full((n, Hkv, 2, D), 99, dtype=torch.int8), torch.full((n, Hkv), 99, dtype=torch.int8)
+    got, got_e = g3.page_bounds(k.to(dev()), gi(table), gi(old), gi(lens), bounds.to(dev()), exps.to(dev()))
+    assert reported() and clean()
+    rows = torch.full((2, n // 2), P)
+    rows[1, -1] = 3
+    for b in range(2):
+        for j in range(n // 2):
+            if (b, j) not in bad:
+                for h in range(Hkv):
+                    bd, e = PG.page_bounds_of(k[int(table[b, j]), h, :int(rows[b, j])])
+                    bounds[int(table[b, j]), h], exps[int(table[b, j]), h] = torch.from_numpy(bd).to(torch.int8), e
+    assert torch.equal(got.cpu(), bounds) and torch.equal(got_e.cpu(), exps)
+
+
 def test_page_bounds_of_non_finite_and_extreme_keys():
     P, D = 16, 64
     k = torch.randn(4, 1, P, D, generator=torch.Generator().manual_seed(2)).bfloat16()
