@@ -356,11 +356,7 @@ cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st) {
 // ============================================================== page bounds
 // HBM-bound: the rows of one (page, kv head) are read once, by one warp or, with
 // few pages, by up to 8 that share them; a lane keeps the largest and smallest
-// value of 8 features in packed bf16.  A page of no more rows than a warp has in
-// flight goes to the D / 8 lanes of one row instead (OWN), so that a warp works
-// on several pages: 36 us against 77 for 200K tokens of 8 kv heads, D = 64, pages
-// of 16 (35 against 42 with pages of 32, 36 against 41 with D = 128); with pages
-// of twice that size both take the same time.
+// value of 8 features in packed bf16.
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsUnroll = 8;  // 16-byte loads in flight per lane
 
@@ -373,7 +369,7 @@ __device__ __forceinline__ int bound_exponent(uint32_t bf16_bits) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
 
-template <int D, bool OWN>
+template <int D>
 __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoundsParams p) {
   extern __shared__ int bounds_smem[];  // [B + 1] touched pages before each sequence
   __shared__ int warp_sums[kBoundsThreads / 32];
@@ -396,17 +392,15 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
   const int P = 1 << p.page_shift;
   constexpr int WARPS = kBoundsThreads / 32;
   int split = 1;  // warps that share a unit's rows
-  while (!OWN && split < WARPS && units <= (int)gridDim.x * WARPS / (2 * split) && split * TPS * kBoundsUnroll < P) split *= 2;
+  while (split < WARPS && units <= (int)gridDim.x * WARPS / (2 * split) && split * TPS * kBoundsUnroll < P) split *= 2;
   const int part = warp % split;
-  constexpr int PER_WARP = OWN ? TPS : 1, ROW_STEP = OWN ? 1 : TPS;
-  const int row0 = OWN ? 0 : sub;
-  for (int u0 = blockIdx.x * (WARPS / split); u0 * PER_WARP < units; u0 += gridDim.x * (WARPS / split)) {
-    const int u = OWN ? (u0 + warp) * TPS + sub : u0 + warp / split, pj = min(u, units - 1) / p.Hkv, h = u % p.Hkv;
+  for (int u0 = blockIdx.x * (WARPS / split); u0 < units; u0 += gridDim.x * (WARPS / split)) {
+    const int u = u0 + warp / split, pj = min(u, units - 1) / p.Hkv, h = u % p.Hkv;
     const int b = find_row(bounds_smem, p.B, pj, 1);
     const int j = (p.old_lens[b] >> p.page_shift) + pj - bounds_smem[b];
     const int page = p.block_table[(size_t)b * p.max_pages + j];
     const bool ok = u < units && page >= 0 && page < p.n_pages;
-    if (u < units && !ok && li == 0) record_error(p.status, kErrInvalid, 321);
+    if (u < units && !ok && lane == 0) record_error(p.status, kErrInvalid, 321);
     const int rows = ok ? min(P, p.seq_lens[b] - (j << p.page_shift)) : 0;
     const uint4* base = reinterpret_cast<const uint4*>(p.k_pages + (((size_t)(ok ? page : 0) * p.Hkv + h) << p.page_shift) * D) + li;
     const __nv_bfloat162 ninf = __floats2bfloat162_rn(-INFINITY, -INFINITY), pinf = __floats2bfloat162_rn(INFINITY, INFINITY);
@@ -416,11 +410,11 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
       mx[i] = ninf;
       mn[i] = pinf;
     }
-    for (int r0 = part * ROW_STEP * kBoundsUnroll; r0 < rows; r0 += split * ROW_STEP * kBoundsUnroll) {
+    for (int r0 = part * TPS * kBoundsUnroll; r0 < rows; r0 += split * TPS * kBoundsUnroll) {
       uint4 x[kBoundsUnroll];
 #pragma unroll
       for (int k = 0; k < kBoundsUnroll; ++k) {
-        const int r = min(r0 + k * ROW_STEP + row0, rows - 1);  // a row read twice changes nothing
+        const int r = min(r0 + k * TPS + sub, rows - 1);  // a row read twice changes nothing
         x[k] = __ldg(base + (size_t)r * LPT);
       }
 #pragma unroll
@@ -433,14 +427,12 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
         }
       }
     }
-    if (!OWN) {
 #pragma unroll
-      for (int off = LPT; off < 32; off <<= 1) {
+    for (int off = LPT; off < 32; off <<= 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __hmax2_nan(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
-          mn[i] = __hmin2_nan(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
-        }
+      for (int i = 0; i < 4; ++i) {
+        mx[i] = __hmax2_nan(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+        mn[i] = __hmin2_nan(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
       }
     }
     if (split > 1) {
@@ -460,7 +452,7 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
           }
       }
     }
-    if (part != 0) continue;
+    if (part != 0 || !ok) continue;
     // Bits of |x| of bf16 values order as integers; a NaN's are above infinity's.
     uint32_t amax = 0;
 #pragma unroll
@@ -486,7 +478,7 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
       hi8[i / 4] |= ((uint32_t)(int)ua & 0xffu) << (8 * (i % 4));
       lo8[i / 4] |= ((uint32_t)(int)uc & 0xffu) << (8 * (i % 4));
     }
-    if (ok && (OWN || sub == 0)) {
+    if (sub == 0) {
       const size_t ph = (size_t)page * p.Hkv + h;
       uint2* dst = reinterpret_cast<uint2*>(p.bounds + ph * 2 * D);
       dst[li] = make_uint2(hi8[0], hi8[1]);
@@ -500,11 +492,10 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
   const long long most = ((long long)p.B * p.max_pages * p.Hkv + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
   const dim3 grid((unsigned)std::min<long long>(most, 148 * 4)), block(kBoundsThreads);
   const size_t smem = (p.B + 1) * sizeof(int);
-  const bool own = (1 << p.page_shift) <= 256 / D * kBoundsUnroll;
   switch (D) {
-    case 64: return launch_dependent(own ? page_bounds_kernel<64, true> : page_bounds_kernel<64, false>, grid, block, smem, st, p);
-    case 128: return launch_dependent(own ? page_bounds_kernel<128, true> : page_bounds_kernel<128, false>, grid, block, smem, st, p);
-    case 256: return launch_dependent(page_bounds_kernel<256, false>, grid, block, smem, st, p);
+    case 64: return launch_dependent(page_bounds_kernel<64>, grid, block, smem, st, p);
+    case 128: return launch_dependent(page_bounds_kernel<128>, grid, block, smem, st, p);
+    case 256: return launch_dependent(page_bounds_kernel<256>, grid, block, smem, st, p);
   }
   return cudaErrorInvalidValue;
 }
@@ -646,6 +637,7 @@ __device__ __forceinline__ void score_pages(const PageSelectParams& p, const int
 
 constexpr int kPickBits = 11, kPickBins = 1 << kPickBits;
 struct PickSmem {
+  uint32_t keys[kKeysInSmem];
   __align__(16) uint32_t hist[kPickBins];  // highest digit first
   uint32_t sums[kSelectWarps], digit, left, count;
   uint32_t lo[kSelectWarps], hi[kSelectWarps];
@@ -777,7 +769,6 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   __shared__ __align__(16) int8_t q8[8 * QueryHead<D>::ROW];
   __shared__ float q_unit[8];
   __shared__ PickSmem pick;
-  extern __shared__ uint32_t smem_keys[];  // the first block's: the scores as ordered integers
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranks = cluster_size(), rank = blockIdx.x % ranks;
   const int turn = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
@@ -811,8 +802,8 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   cluster_wait();
   const int32_t* table = p.block_table + (size_t)b * p.max_pages;
   uint32_t* keys = p.keys + (size_t)pair * p.max_pages;
-  const bool in_smem = np <= p.keys_in_smem;
-  const uint32_t first_keys = cluster_address(smem_keys, 0);
+  const bool in_smem = np <= kKeysInSmem;
+  const uint32_t first_keys = cluster_address(pick.keys, 0);
   score_pages<D>(p, table, h, np, (rank * kSelectWarps + warp) * 16, np, ranks * kSelectWarps * 16, q8, q_unit,
                  [&](int j, uint32_t key) {
                    if (in_smem)
@@ -824,7 +815,7 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   if (rank != 0) return;
   cluster_wait();
   if (in_smem)
-    write_pages([&](int i) { return smem_keys[i]; }, np, p.n_select, out, pick);
+    write_pages([&](int i) { return pick.keys[i]; }, np, p.n_select, out, pick);
   else  // other blocks wrote them: read where they are written, in L2
     write_pages([&](int i) { return __ldcg(keys + i); }, np, p.n_select, out, pick);
 }
@@ -838,11 +829,7 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
   p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= kSelectThreads;
-  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence take 22 us so and 33 with
-  // their scores in L2, while 32 KB for every call would cost the short ones 0.4 us and the batch above 4.
-  p.keys_in_smem = std::min(p.max_pages, kKeysInSmem);
   cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = p.keys_in_smem * sizeof(uint32_t);
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
   cfg.blockDim = dim3(kSelectThreads);
   cfg.stream = st;
