@@ -234,7 +234,7 @@ struct PageBoundsParams {
 };
 cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st);
 
-constexpr int kKeysInSmem = 4096;  // page scores that a block keeps in shared memory
+constexpr int kKeysInSmem = 8192;  // page scores that a block keeps in shared memory at most
 struct PageSelectParams {
   const __nv_bfloat16* q_hat;  // [B, Hq, D]
   const int8_t* bounds;
@@ -245,7 +245,8 @@ struct PageSelectParams {
   int32_t* pages;  // [B, Hkv, n_select]
   int* status;
   int B, max_pages, Hq, Hkv, G, page_shift, n_pages, n_select;
-  int by_length;  // set by the launcher: blocks take the long sequences first
+  int by_length;     // set by the launcher: blocks take the long sequences first
+  int keys_in_smem;  // set by the launcher: scores that find room in shared memory
 };
 cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st);
 

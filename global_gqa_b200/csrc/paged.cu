@@ -646,7 +646,6 @@ __device__ __forceinline__ void score_pages(const PageSelectParams& p, const int
 
 constexpr int kPickBits = 11, kPickBins = 1 << kPickBits;
 struct PickSmem {
-  uint32_t keys[kKeysInSmem];
   __align__(16) uint32_t hist[kPickBins];  // highest digit first
   uint32_t sums[kSelectWarps], digit, left, count;
   uint32_t lo[kSelectWarps], hi[kSelectWarps];
@@ -778,6 +777,7 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   __shared__ __align__(16) int8_t q8[8 * QueryHead<D>::ROW];
   __shared__ float q_unit[8];
   __shared__ PickSmem pick;
+  extern __shared__ uint32_t smem_keys[];  // the first block's: the scores as ordered integers
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranks = cluster_size(), rank = blockIdx.x % ranks;
   const int turn = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   cluster_wait();
   const int32_t* table = p.block_table + (size_t)b * p.max_pages;
   uint32_t* keys = p.keys + (size_t)pair * p.max_pages;
-  const bool in_smem = np <= kKeysInSmem;
-  const uint32_t first_keys = cluster_address(pick.keys, 0);
+  const bool in_smem = np <= p.keys_in_smem;
+  const uint32_t first_keys = cluster_address(smem_keys, 0);
   score_pages<D>(p, table, h, np, (rank * kSelectWarps + warp) * 16, np, ranks * kSelectWarps * 16, q8, q_unit,
                  [&](int j, uint32_t key) {
                    if (in_smem)
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   if (rank != 0) return;
   cluster_wait();
   if (in_smem)
-    write_pages([&](int i) { return pick.keys[i]; }, np, p.n_select, out, pick);
+    write_pages([&](int i) { return smem_keys[i]; }, np, p.n_select, out, pick);
   else  // other blocks wrote them: read where they are written, in L2
     write_pages([&](int i) { return __ldcg(keys + i); }, np, p.n_select, out, pick);
 }
@@ -838,7 +838,11 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
   p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= kSelectThreads;
+  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence take 22 us so and 33 with
+  // their scores in L2, while 32 KB for every call would cost the short ones 0.4 us and the batch above 4.
+  p.keys_in_smem = std::min(p.max_pages, kKeysInSmem);
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = p.keys_in_smem * sizeof(uint32_t);
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
   cfg.blockDim = dim3(kSelectThreads);
   cfg.stream = st;

@@ -310,11 +310,11 @@ def test_page_select_longest():
     """More pages than a block keeps the scores of: ties and a long list."""
     P, D, n = 16, 64, 1500
     rng, g = np.random.default_rng(8), torch.Generator().manual_seed(8)
-    lens = [6000 * P, 4096 * P, 4097 * P - 3, 100]
+    lens = [9000 * P, 6000 * P, 4096 * P, 4097 * P - 3, 8192 * P, 8193 * P - 3, 100]
     table, n_pages = scattered(rng, lens, P)
     bounds = torch.randint(-9, 10, (n_pages, 1, 2, D), generator=g).to(torch.int8)
-    check_select(torch.randn(4, 2, D, generator=g).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
-    check_select(torch.zeros(4, 2, D).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
+    check_select(torch.randn(len(lens), 2, D, generator=g).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
+    check_select(torch.zeros(len(lens), 2, D).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
     assert clean()
 
 

@@ -80,8 +80,8 @@ def test_no_tokens_is_no_work(lib):
 
 
 def test_workspace_sizes(lib):
-    assert 0 < lib.g3attn_page_select_workspace_size(64, 16, 4096) <= 4096  # scores stay on chip
-    assert lib.g3attn_page_select_workspace_size(64, 16, 8192) == 64 * 16 * 8192 * 4
+    assert 0 < lib.g3attn_page_select_workspace_size(64, 16, 8192) <= 4096  # scores stay on chip
+    assert lib.g3attn_page_select_workspace_size(64, 16, 8193) == 64 * 16 * 8193 * 4
     assert lib.g3attn_page_select_workspace_size(0, 16, 2048) == 0
     # two partial softmaxes per block, whatever the batch and the lengths
     assert lib.g3attn_paged_decode_workspace_size(96) == 0 and lib.g3attn_paged_decode_workspace_size(128) >= 2 * 148 * 8 * 128 * 4
