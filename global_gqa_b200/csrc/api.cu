@@ -1106,7 +1106,7 @@ g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void
   p.kind = (int)layer_kind;
   p.window = window;
   p.n_blocks = g3::paged_decode_blocks(D);
-// With 8 or more blocks per pair, the unequal shares of dealt blocks (at most an eighth) cost less than
+  // With 8 or more blocks per pair, the unequal shares of dealt blocks (at most an eighth) cost less than
   // a block's second pass for the pair it shares with its neighbour (2 of 11 us at one sequence of 4K tokens).
   p.deal = (long long)B * Hkv * 8 <= p.n_blocks ? 1 : 0;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));

@@ -529,9 +529,6 @@ cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, cudaStream_t st
 // its first block, which picks behind the cluster's barrier: the scores as ordered
 // integers, the threshold by 11-bit digits below the highest bit in which they
 // differ, then an ordered write.
-constexpr int kSelectThreads = 256;
-constexpr int kSelectWarps = kSelectThreads / 32;
-
 __device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -645,21 +642,23 @@ __device__ __forceinline__ void score_pages(const PageSelectParams& p, const int
 }
 
 constexpr int kPickBits = 11, kPickBins = 1 << kPickBits;
+template <int THREADS>
 struct PickSmem {
   __align__(16) uint32_t hist[kPickBins];  // highest digit first
-  uint32_t sums[kSelectWarps], digit, left, count;
-  uint32_t lo[kSelectWarps], hi[kSelectWarps];
-  int gt[kSelectWarps], eq[kSelectWarps];
+  uint32_t sums[THREADS / 32], digit, left, count;
+  uint32_t lo[THREADS / 32], hi[THREADS / 32];
+  int gt[THREADS / 32], eq[THREADS / 32];
 };
 
 // The k highest of n keys (0 < k < n), equal ones by the lower index, in ascending
 // order of the index, by the whole block.
-template <class Key>
-__device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out, PickSmem& sm) {
+template <int THREADS, class Key>
+__device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out, PickSmem<THREADS>& sm) {
+  constexpr int WARPS = THREADS / 32, PER = kPickBins / THREADS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll 4
-  for (int i = tid; i < n; i += kSelectThreads) {
+  for (int i = tid; i < n; i += THREADS) {
     const uint32_t u = key(i);
     lo = min(lo, u);
     hi = max(hi, u);
@@ -670,12 +669,13 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
     sm.lo[warp] = lo;
     sm.hi[warp] = hi;
   }
-  // Bins tid * 8 .. tid * 8 + 7 of the histogram belong to this thread.
-  uint4* mine = reinterpret_cast<uint4*>(sm.hist) + 2 * tid;
-  mine[0] = mine[1] = make_uint4(0u, 0u, 0u, 0u);
+  // PER bins of the histogram from tid * PER on belong to this thread.
+  uint32_t* mine = sm.hist + PER * tid;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     lo = min(lo, sm.lo[w]);
     hi = max(hi, sm.hi[w]);
   }
@@ -685,14 +685,17 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
   while (shift > 0) {
     const int next = max(shift - kPickBits, 0), bits = shift - next;
 #pragma unroll 4
-    for (int i = tid; i < n; i += kSelectThreads) {
+    for (int i = tid; i < n; i += THREADS) {
       const uint32_t u = key(i) - lo;
       if (shift == 32 || (u >> shift) == prefix) atomicAdd(&sm.hist[kPickBins - 1 - ((u >> next) & ((1u << bits) - 1u))], 1u);
     }
     __syncthreads();
-    const uint4 d0 = mine[0], d1 = mine[1];
-    const uint32_t d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-    const uint32_t sum = d[0] + d[1] + d[2] + d[3] + d[4] + d[5] + d[6] + d[7];
+    uint32_t d[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      d[i] = mine[i];
+      sum += d[i];
+    }
     uint32_t before = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -700,17 +703,18 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
       if (lane >= off) before += v;
     }
     if (lane == 31) sm.sums[warp] = before;
-    mine[0] = mine[1] = make_uint4(0u, 0u, 0u, 0u);  // for a finer digit
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[i] = 0;  // for a finer digit
     __syncthreads();
     before -= sum;
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) before += w < warp ? sm.sums[w] : 0u;
+    for (int w = 0; w < WARPS; ++w) before += w < warp ? sm.sums[w] : 0u;
     if (before < left && before + sum >= left) {  // one thread: the digit at which the count from above reaches `left`
       uint32_t digit = 0, count = 0, taken = before;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < PER; ++i) {
         if (before < left) {
-          digit = kPickBins - 1 - (tid * 8 + i);
+          digit = kPickBins - 1 - (tid * PER + i);
           count = d[i];
           taken = before;
         }
@@ -726,7 +730,7 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
     shift = next;
     if (sm.count == left) break;  // all of them are taken: no finer threshold is needed
   }
-  const int per = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
+  const int per = ((n + WARPS - 1) / WARPS + 31) / 32 * 32, i0 = min(n, warp * per), i1 = min(n, i0 + per);
   int gt = 0, eq = 0;
 #pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
@@ -761,23 +765,25 @@ __device__ __forceinline__ void pick_pages(Key&& key, int n, int k, int32_t* out
 }
 
 // The newest page, and the picked ones before it.
-template <class Key>
-__device__ __forceinline__ void write_pages(Key&& key, int np, int n_select, int32_t* out, PickSmem& sm) {
+template <int THREADS, class Key>
+__device__ __forceinline__ void write_pages(Key&& key, int np, int n_select, int32_t* out, PickSmem<THREADS>& sm) {
   if (threadIdx.x == 0) out[n_select - 1] = np - 1;
   if (n_select > 1) pick_pages(key, np - 1, n_select - 1, out, sm);
 }
 
 // A sequence without a choice: all its pages.
+template <int THREADS>
 __device__ __forceinline__ void write_all(int np, int n_select, int32_t* out) {
-  for (int i = threadIdx.x; i < n_select; i += kSelectThreads) out[i] = i < np ? i : -1;
+  for (int i = threadIdx.x; i < n_select; i += THREADS) out[i] = i < np ? i : -1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_kernel(PageSelectParams p) {
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 1024) / THREADS) page_select_kernel(PageSelectParams p) {
   __shared__ __align__(16) int8_t q8[8 * QueryHead<D>::ROW];
   __shared__ float q_unit[8];
-  __shared__ PickSmem pick;
+  __shared__ PickSmem<THREADS> pick;
   extern __shared__ uint32_t smem_keys[];  // the first block's: the scores as ordered integers
+  constexpr int WARPS = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranks = cluster_size(), rank = blockIdx.x % ranks;
   const int turn = blockIdx.x / ranks / p.Hkv, h = blockIdx.x / ranks % p.Hkv;
@@ -787,7 +793,7 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   griddep_launch();
   if (p.by_length) {
     // The `turn`-th longest sequence: the blocks that start last have the least to do.
-    __shared__ int s_len[kSelectThreads], s_b;
+    __shared__ int s_len[THREADS], s_b;
     const int t = threadIdx.x, mine = t < p.B ? p.seq_lens[t] : 0;
     s_len[t] = mine;
     __syncthreads();
@@ -799,21 +805,21 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
   }
   const int pair = b * p.Hkv + h;
   QueryHead<D> head;
-  head.load(p, b, h, warp, lane);  // on its way while the length is read
+  if (warp < 8) head.load(p, b, h, warp, lane);  // on its way while the length is read
   const int np = pages_of(p, b, rank == 0 && threadIdx.x == 0);
   int32_t* out = p.pages + (size_t)pair * p.n_select;
   if (np <= p.n_select) {  // the same for the whole cluster
-    if (rank == 0) write_all(np, p.n_select, out);
+    if (rank == 0) write_all<THREADS>(np, p.n_select, out);
     return;
   }
-  head.store(q8, q_unit, warp, lane);
+  if (warp < 8) head.store(q8, q_unit, warp, lane);
   __syncthreads();
   cluster_wait();
   const int32_t* table = p.block_table + (size_t)b * p.max_pages;
   uint32_t* keys = p.keys + (size_t)pair * p.max_pages;
   const bool in_smem = np <= p.keys_in_smem;
   const uint32_t first_keys = cluster_address(smem_keys, 0);
-  score_pages<D>(p, table, h, np, (rank * kSelectWarps + warp) * 16, np, ranks * kSelectWarps * 16, q8, q_unit,
+  score_pages<D>(p, table, h, np, (rank * WARPS + warp) * 16, np, ranks * WARPS * 16, q8, q_unit,
                  [&](int j, uint32_t key) {
                    if (in_smem)
                      cluster_store(first_keys + 4 * j, key);
@@ -829,22 +835,23 @@ __global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_select_
     write_pages([&](int i) { return __ldcg(keys + i); }, np, p.n_select, out, pick);
 }
 
-template <int D>
+template <int D, int THREADS>
 static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   const long long pairs = (long long)p.B * p.Hkv;
+  constexpr int WARPS = THREADS / 32;
   // Blocks per pair: up to 8, at least 16 pages for each of their warps, no more than find a place at once.
   int ranks = 1;
-  while (ranks < 8 && ranks * kSelectWarps * 16 < p.max_pages && pairs * ranks < 148 * 2) ranks *= 2;
+  while (ranks < 8 && ranks * WARPS * 16 < p.max_pages && pairs * ranks < 148 * 2) ranks *= 2;
   // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
-  p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= kSelectThreads;
-  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence take 22 us so and 33 with
+  p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= THREADS;
+  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence take 18 us so and 29 with
   // their scores in L2, while 32 KB for every call would cost the short ones 0.4 us and the batch above 4.
   p.keys_in_smem = std::min(p.max_pages, kKeysInSmem);
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = p.keys_in_smem * sizeof(uint32_t);
   cfg.gridDim = dim3((unsigned)(pairs * ranks));
-  cfg.blockDim = dim3(kSelectThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -854,15 +861,19 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, page_select_kernel<D>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, page_select_kernel<D, THREADS>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st) {
+  // Blocks of 512 threads where every cluster of 8 finds an SM for each of its blocks: the pick, by one block, takes half
+  // the time.  One sequence and 16 kv heads of D = 128: 7.4 us against 8.0 at 2048 pages, 18.3 against 22.1 at 8192, 6.3
+  // against 6.7 at 1024; at two blocks per SM (two such sequences) 11.2 against 9.2.
+  const bool wide = (long long)p.B * p.Hkv * 8 <= 148 && p.max_pages >= 1024;
   switch (D) {
-    case 64: return launch_select_d<64>(p, st);
-    case 128: return launch_select_d<128>(p, st);
-    case 256: return launch_select_d<256>(p, st);
+    case 64: return wide ? launch_select_d<64, 512>(p, st) : launch_select_d<64, 256>(p, st);
+    case 128: return wide ? launch_select_d<128, 512>(p, st) : launch_select_d<128, 256>(p, st);
+    case 256: return wide ? launch_select_d<256, 512>(p, st) : launch_select_d<256, 256>(p, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
     __syncthreads();
     // A block's first part goes to its slot 0; one that begins behind another pair's end to slot 1.
     const int slot = 2 * blockIdx.x + (!p.deal && range0 < g0 ? 1 : 0);
-if (!whole && first == 0) cut = make_int4(pair, blockIdx.x, p.deal ? blockIdx.x + dealt - 1 : sh.owner(g_pair - 1), slot);
+    if (!whole && first == 0) cut = make_int4(pair, blockIdx.x, p.deal ? blockIdx.x + dealt - 1 : sh.owner(g_pair - 1), slot);
     if (p.deal && first == 0 && tid == 0) p.cuts[pair] = cut;
     for (int v = tid; v < p.G * (D / 4); v += kPagedThreads) {
       const int gh = v / (D / 4), f = v % (D / 4) * 4;

@@ -318,6 +318,22 @@ def test_page_select_longest():
     assert clean()
 
 
+@pytest.mark.parametrize("D,Hkv,G,n", [(64, 4, 8, 7), (128, 8, 2, 64), (256, 3, 5, 1000), (128, 1, 1, 2)])
+def test_page_select_few_long_sequences(D, Hkv, G, n):
+    """Block tables of 1024 pages and more for few pairs; a short sequence beside the long one, equal scores in long runs."""
+    P = 32
+    rng, g = np.random.default_rng(D), torch.Generator().manual_seed(D)
+    for lens in ([1024 * P], [2500 * P - 7, n * P], [1500 * P + 1, (n + 1) * P]):
+        table, n_pages = scattered(rng, lens, P)
+        q = torch.randn(len(lens), Hkv * G, D, generator=g).bfloat16()
+        bounds = torch.randint(-127, 128, (n_pages, Hkv, 2, D), generator=g).to(torch.int8)
+        exps = torch.randint(2, 6, (n_pages, Hkv), generator=g).to(torch.int8)
+        check_select(q, bounds, exps, table, lens, P, n)
+        bounds[torch.from_numpy(rng.permutation(n_pages)[:n_pages // 2])] = 5
+        check_select(q, bounds, exps * 0 + 3, table, lens, P, n)
+    assert clean()
+
+
 @pytest.mark.parametrize("B", [100, 256, 300])
 def test_page_select_many_sequences(B):
     """More pairs than find a place at once: taken by length, up to 256 sequences, equal and idle ones among them."""
