@@ -845,8 +845,8 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
   p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= THREADS;
-  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence take 18 us so and 29 with
-  // their scores in L2, while 32 KB for every call would cost the short ones 0.4 us and the batch above 4.
+  // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence took 22 us so and 33 with
+  // their scores in L2 (blocks of 256), while 32 KB for every call cost the short ones 0.4 us and the batch above 4.
   p.keys_in_smem = std::min(p.max_pages, kKeysInSmem);
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = p.keys_in_smem * sizeof(uint32_t);
@@ -867,8 +867,8 @@ static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
 
 cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st) {
   // Blocks of 512 threads where every cluster of 8 finds an SM for each of its blocks: the pick, by one block, takes half
-  // the time.  One sequence and 16 kv heads of D = 128: 7.4 us against 8.0 at 2048 pages, 18.3 against 22.1 at 8192, 6.3
-  // against 6.7 at 1024; at two blocks per SM (two such sequences) 11.2 against 9.2.
+  // the time.  One sequence with 16 kv heads of D = 128: 6.3 us against 6.7 at 1024 pages, 18-20 against 22 at 8192; with
+  // one of D = 256 7.4 against 8.0 at 2048, 34 against 48 at 16384.  Two blocks per SM (32 pairs, 2048 pages): 11.2 against 9.2.
   const bool wide = (long long)p.B * p.Hkv * 8 <= 148 && p.max_pages >= 1024;
   switch (D) {
     case 64: return wide ? launch_select_d<64, 512>(p, st) : launch_select_d<64, 256>(p, st);
