@@ -227,8 +227,13 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAppendParams p) {
+//
+// FEW: a warp has one share of one token (one turn of the loop), V's rows are rows of their own, and the first loads
+// go out before anything else is read: a step's call is bound by the reads that wait for one another.  With many
+// tokens the registers that this takes (80 for 64) cost more than it gives: 3.9 us against 3.7 for 256 tokens of
+// 32/16 heads, D = 128, 10.5 against 8.5 for 1024; 64 tokens take 2.75 against 3.3.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kAppendThreads, FEW ? 3 : 4) paged_append_kernel(PagedAppendParams p) {
   constexpr int H2 = D / 2;
   constexpr int LPR = D / 16;    // lanes per row: each holds 8 features of each half
   constexpr int RPW = 32 / LPR;  // rows per warp step
@@ -239,24 +244,49 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
   const int li = lane % LPR, sub = lane / LPR;
   const int d1 = li * 8;
   const int heads = p.Hq + p.Hkv;  // Hq = 0 without queries
-  for (int i = threadIdx.x; i < H2; i += kAppendThreads) inv_freq_s[i] = p.inv_freq[i];
-  const uint32_t token = griddep_wait_token();
-  griddep_launch();
-  for (int i = threadIdx.x; i < 2 * D; i += kAppendThreads)
-    gam[i] = i >= D ? p.k_gamma[i - D] : p.Hq > 0 ? p.q_gamma[i] : 0.f;
-  __syncthreads();
-
+  const int rows = FEW ? heads + p.Hkv : heads;
   // `share` of a token's rows: 2^warps_shift warps split them.
   const int warps_per_token = 1 << p.warps_shift;
   const long long items = (long long)p.T << p.warps_shift;
   const long long stride = (long long)gridDim.x * (kAppendThreads / 32);
-  for (long long it = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); it < items; it += stride) {
+  long long it = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  for (int i = threadIdx.x; i < H2; i += kAppendThreads) inv_freq_s[i] = p.inv_freq[i];
+  const uint32_t token = griddep_wait_token();
+  griddep_launch();
+  uint4 xa[kAppendUnroll], xb[kAppendUnroll];
+  auto load = [&](int t, int h0, bool keep) {
+    const __nv_bfloat16* qrow = p.q + (size_t)t * p.Hq * D;
+    const __nv_bfloat16* krow = p.k + (size_t)t * p.Hkv * D;
+    const __nv_bfloat16* vrow = p.v + (size_t)t * p.Hkv * D;
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+      const int h = h0 + u * RPW + sub;
+      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < rows && (h < p.Hq || keep)) {
+        const __nv_bfloat16* src = h < p.Hq ? qrow + h * D : !FEW || h < heads ? krow + (h - p.Hq) * D : vrow + (h - heads) * D;
+        xa[u] = ldg_after(src + d1, token);
+        xb[u] = ldg_after(src + H2 + d1, token);
+      }
+    }
+  };
+  if (FEW && it < items) load((int)(it >> p.warps_shift), ((int)it & (warps_per_token - 1)) * RPW * kAppendUnroll, true);
+  int slot = 0, position = 0;
+  auto place = [&]() {
+    slot = p.slots[it >> p.warps_shift];
+    position = p.positions[it >> p.warps_shift];
+  };
+  if (FEW && it < items) place();
+  for (int i = threadIdx.x; i < 2 * D; i += kAppendThreads)
+    gam[i] = i >= D ? p.k_gamma[i - D] : p.Hq > 0 ? p.q_gamma[i] : 0.f;
+  __syncthreads();
+
+  for (; it < items; it += stride) {
     const int t = (int)(it >> p.warps_shift), share = (int)it & (warps_per_token - 1);
-    const int slot = p.slots[t];
+    if (!FEW) place();
     const bool keep = slot >= 0 && slot < p.n_slots;
     if (slot >= p.n_slots && lane == 0 && share == 0) record_error(p.status, kErrInvalid, 310);
     float cl[FPL], sl[FPL];
-    const double pos = (double)p.positions[t] / p.interp;
+    const double pos = (double)position / p.interp;
 #pragma unroll
     for (int i = 0; i < FPL; ++i) {
       const int f = FPL * lane + i;
@@ -278,20 +308,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
     // First row of the slot: rows of one (page, head) are P apart from the next head's.
     const size_t page = keep ? (size_t)(slot >> p.page_shift) : 0;
     const size_t crow0 = ((page * p.Hkv) << p.page_shift) + (keep ? slot & ((1 << p.page_shift) - 1) : 0);
-    const __nv_bfloat16* qrow = p.q + (size_t)t * p.Hq * D;
-    const __nv_bfloat16* krow = p.k + (size_t)t * p.Hkv * D;
-    for (int h0 = share * RPW * kAppendUnroll; h0 < heads; h0 += warps_per_token * RPW * kAppendUnroll) {
-      uint4 xa[kAppendUnroll], xb[kAppendUnroll];
-#pragma unroll
-      for (int u = 0; u < kAppendUnroll; ++u) {
-        const int h = h0 + u * RPW + sub;
-        xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < heads && (h < p.Hq || keep)) {
-          const __nv_bfloat16* src = h < p.Hq ? qrow + h * D : krow + (h - p.Hq) * D;
-          xa[u] = ldg_after(src + d1, token);
-          xb[u] = ldg_after(src + H2 + d1, token);
-        }
-      }
+    const int first = share * RPW * kAppendUnroll;
+    for (int h0 = first; h0 < rows; h0 += warps_per_token * RPW * kAppendUnroll) {
+      if (!FEW || h0 != first) load(t, h0, keep);
 #pragma unroll
       for (int u = 0; u < kAppendUnroll; ++u) {
         float x[16];
@@ -303,7 +322,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
 #pragma unroll
         for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
         const int h = h0 + u * RPW + sub;
-        if (h >= heads || (h >= p.Hq && !keep)) continue;
+        if (h >= rows || (h >= p.Hq && !keep)) continue;
+        if (FEW && h >= heads) {
+          const size_t at = (crow0 + ((size_t)(h - heads) << p.page_shift)) * D;
+          *reinterpret_cast<uint4*>(p.v_pages + at + d1) = xa[u];
+          *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = xb[u];
+          continue;
+        }
         const bool is_q = h < p.Hq;
         const float rinv = rsqrtf(ss * (1.0f / D) + 1e-6f);
         const float* gs = gam + (is_q ? 0 : D);
@@ -329,9 +354,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
           const size_t at = (crow0 + ((size_t)kh << p.page_shift)) * D;
           *reinterpret_cast<uint4*>(p.k_pages + at + d1) = pack8(o);
           *reinterpret_cast<uint4*>(p.k_pages + at + H2 + d1) = pack8(o + 8);
-          const __nv_bfloat16* vsrc = p.v + ((size_t)t * p.Hkv + kh) * D;
-          *reinterpret_cast<uint4*>(p.v_pages + at + d1) = ldg_after(vsrc + d1, token);
-          *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = ldg_after(vsrc + H2 + d1, token);
+          if (!FEW) {
+            const __nv_bfloat16* vsrc = p.v + ((size_t)t * p.Hkv + kh) * D;
+            *reinterpret_cast<uint4*>(p.v_pages + at + d1) = ldg_after(vsrc + d1, token);
+            *reinterpret_cast<uint4*>(p.v_pages + at + H2 + d1) = ldg_after(vsrc + H2 + d1, token);
+          }
         }
       }
     }
@@ -339,16 +366,23 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(PagedAp
 }
 
 cudaError_t launch_paged_append(PagedAppendParams p, int D, cudaStream_t st) {
-  // A few tokens: split each one's rows over more warps, up to one step of rows each.
-  const int rows_step = 32 / (D / 16) * kAppendUnroll, heads = p.Hq + p.Hkv;
-  p.warps_shift = 0;
-  while (p.warps_shift < 3 && (rows_step << p.warps_shift) < heads && ((long long)p.T << p.warps_shift) < 148 * 16) ++p.warps_shift;
-  const long long items = (long long)p.T << p.warps_shift;
-  const unsigned blocks = (unsigned)std::min<long long>((items + kAppendThreads / 32 - 1) / (kAppendThreads / 32), 148 * 8);
+  // A few tokens: split each one's rows over up to 8 warps, as long as each has a step of rows.
+  const int rows_step = 32 / (D / 16) * kAppendUnroll;
+  auto split = [&](int rows) {
+    int shift = 0;
+    while (shift < 3 && (rows_step << shift) < rows && ((long long)p.T << shift) < 148 * 16) ++shift;
+    return shift;
+  };
+  p.warps_shift = split(p.Hq + 2 * p.Hkv);
+  // FEW (see there) while one block per SM holds them.
+  const bool few = (long long)p.T << p.warps_shift <= 148 * (kAppendThreads / 32);
+  if (!few) p.warps_shift = split(p.Hq + p.Hkv);
+  const long long blocks = (((long long)p.T << p.warps_shift) + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const dim3 grid((unsigned)std::min<long long>(blocks, 148 * 8));
   switch (D) {
-    case 64: return launch_dependent(paged_append_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
-    case 128: return launch_dependent(paged_append_kernel<128>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
-    case 256: return launch_dependent(paged_append_kernel<256>, dim3(blocks), dim3(kAppendThreads), 0, st, p);
+    case 64: return launch_dependent(few ? paged_append_kernel<64, true> : paged_append_kernel<64, false>, grid, dim3(kAppendThreads), 0, st, p);
+    case 128: return launch_dependent(few ? paged_append_kernel<128, true> : paged_append_kernel<128, false>, grid, dim3(kAppendThreads), 0, st, p);
+    case 256: return launch_dependent(few ? paged_append_kernel<256, true> : paged_append_kernel<256, false>, grid, dim3(kAppendThreads), 0, st, p);
   }
   return cudaErrorInvalidValue;
 }

@@ -135,6 +135,7 @@ def near_rotated(got, x, gamma, pos, base, interp):
 @pytest.mark.parametrize("T,Hq,Hkv,D,P", [
     (1, 4, 2, 64, 16), (5, 32, 16, 128, 64), (64, 32, 16, 128, 64), (300, 4, 1, 256, 32), (64, 4, 1, 256, 128),
     (33, 24, 8, 128, 256), (700, 15, 3, 64, 16), (5000, 2, 2, 64, 128), (2400, 8, 1, 128, 16),
+    (9, 40, 20, 128, 32), (21, 48, 9, 256, 16), (148, 64, 8, 128, 16), (149, 33, 16, 128, 64), (1184, 2, 1, 128, 16), (1185, 2, 1, 64, 16),
 ])
 @pytest.mark.parametrize("with_q", [True, False])
 def test_paged_append(T, Hq, Hkv, D, P, with_q):
