@@ -59,6 +59,28 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
+// The prefix sums below of n <= 32 * PER terms, by every warp for itself, all writing the same values: no barrier.
+template <int PER, class F>
+__device__ __forceinline__ void warp_prefix(int n, int* pref, F&& count) {
+  const int lane = threadIdx.x & 31, first = PER * lane;
+  int v[PER], sum = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) v[k] = first + k < n ? count(first + k) : 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) v[k] = sum += v[k];
+  int inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += x;
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+    if (first + k < n) pref[first + k + 1] = inc - sum + v[k];
+  if (lane == 0) pref[0] = 0;
+  __syncwarp();
+}
+
 // Inclusive prefix sums of count(b), b < n, into pref[1 .. n], pref[0] = 0, by
 // the whole block (a multiple of 32 threads; `warp_sums` holds one int per
 // warp).  Every block of a grid repeats it: some microseconds at the largest n, for
@@ -66,18 +88,8 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 template <class F>
 __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F&& count) {
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  if (n <= 32) {  // every warp for itself, writing the same values: no barrier
-    int inc = lane < n ? count(lane) : 0;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += v;
-    }
-    if (lane < n) pref[lane + 1] = inc;
-    if (lane == 0) pref[0] = 0;
-    __syncwarp();
-    return;
-  }
+  if (n <= 32) return warp_prefix<1>(n, pref, count);
+  if (n <= 128) return warp_prefix<4>(n, pref, count);  // 0.6 us less than below for 64 sequences
   // The terms first, in coalesced reads that do not wait for one another; then each thread sums a run of its own (of odd
   // length: the threads' runs begin in different banks).  8192 sequences: 12 us, 90 with the reads in the runs.
 #pragma unroll 8
