@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
   long long r = -1, r_next = -1;
   // Goes on to the next pair from unit g on that this warp has a part in, and enters it: its queries and the
   // warp's first keys are on their way.  A pair is worked on by all warps of the block together, unless it is a
-  // small part of the block's share: then by one of them, in turn, without a barrier.
+  // small part of the block's share, or of one or two units: then by one of them, in turn, without a barrier (1024
+  // pairs of up to 256 tokens: 188 us against 296; of one token: 6.9 against 11.6).
   int step = kPagedWarps, turn = 0;
   auto enter = [&](int g) {
     for (; g < range1; g += n) {
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
       h = rel / n;
       i0 = rel - h * n;
       i1 = min(n, i0 + (range1 - g));
-      step = i1 - i0 == n && n <= (range1 - range0) / 16 ? 1 : kPagedWarps;
+      step = i1 - i0 == n && n < range1 - range0 && n <= max((range1 - range0) / 16, 2) ? 1 : kPagedWarps;
       if (step == kPagedWarps || (turn++ & (kPagedWarps - 1)) == warp) break;
     }
     if (g >= range1) return g;
