@@ -461,6 +461,14 @@ def test_paged_decode_many_short(D, Hkv, G, P):
     assert clean()
 
 
+@pytest.mark.parametrize("B,hi", [(64, 18), (64, 70), (70, 130), (33, 33), (300, 50)])
+@pytest.mark.parametrize("D,Hkv,G", [(64, 12, 2), (128, 16, 1), (256, 7, 8)])
+def test_paged_decode_shares_of_few_pairs(B, hi, D, Hkv, G):
+    """Blocks with a few pairs of one unit of 16 tokens, of two and of more, whole ones and cut ones, in any order."""
+    run_decode(decode_case(np.random.default_rng(B + hi).integers(1, hi, B), Hkv * G, Hkv, D, 16, 6))
+    assert clean()
+
+
 @pytest.mark.parametrize("D,Hkv,G,P", SHAPES[::3])
 @pytest.mark.parametrize("W", [1, 7, 16, 100, 1024, 5000])
 def test_paged_decode_window(D, Hkv, G, P, W):
