@@ -35,6 +35,12 @@ constexpr int kMapThreads = 1024;
 // enough for any lengths (cap < 2^31).
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap) { return min(a + b, cap); }
 
+// The same of a warp's 32 terms.
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v, uint32_t cap) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, v & 0xffffu), hi = __reduce_add_sync(0xffffffffu, v >> 16);
+  return (uint32_t)min(((unsigned long long)hi << 16) + lo, (unsigned long long)cap);
+}
+
 template <int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
   extern __shared__ int map_smem[];
@@ -75,10 +81,9 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
     }
     if (lane == 31) s_rows[warp] = rows;
     __syncthreads();
-    uint32_t add = rows_before;
-    for (int w = 0; w < warp; ++w) add = sat_add(add, s_rows[w], cap);
-    rows = sat_add(rows, add, cap);
-    for (int w = 0; w < warps; ++w) rows_before = sat_add(rows_before, s_rows[w], cap);
+    const uint32_t warp_rows = lane < warps ? s_rows[lane] : 0u;
+    rows = sat_add(rows, sat_add(rows_before, warp_sum(lane < warp ? warp_rows : 0u, cap), cap), cap);
+    rows_before = sat_add(rows_before, warp_sum(warp_rows, cap), cap);
 
     const bool valid = b < p.B && old_len >= 0 && new_len >= 0 && (long long)old_len + new_len <= room && rows < cap;
     const int have = valid ? (old_len + p.page_size - 1) >> p.page_shift : 0;
@@ -91,9 +96,9 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
     }
     if (lane == 31) s_need[warp] = c;
     __syncthreads();
-    c += need_before;
-    for (int w = 0; w < warp; ++w) c += s_need[w];
-    for (int w = 0; w < warps; ++w) need_before += s_need[w];
+    const int warp_need = lane < warps ? s_need[lane] : 0;
+    c += need_before + __reduce_add_sync(0xffffffffu, lane < warp ? warp_need : 0);
+    need_before += __reduce_add_sync(0xffffffffu, warp_need);
     if (b < p.B) {
       ends[b] = rows;
       cum[b] = c;
