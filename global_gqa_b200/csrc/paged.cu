@@ -66,12 +66,17 @@ __global__ void __launch_bounds__(THREADS) page_map_kernel(PageMapParams p) {
   // Rows first: whether a request fits the token buffer decides whether it asks for pages.
   uint32_t rows_before = 0;
   int need_before = 0;
+  int next_old = 0, next_new = 0;
+  if (tid < p.B) {
+    next_old = p.old_lens[tid];
+    next_new = p.new_lens[tid];
+  }
   for (int b0 = 0; b0 < p.B; b0 += threads) {
-    const int b = b0 + tid;
-    int old_len = 0, new_len = 0;
-    if (b < p.B) {
-      old_len = p.old_lens[b];
-      new_len = p.new_lens[b];
+    const int b = b0 + tid, old_len = next_old, new_len = next_new;
+    next_old = next_new = 0;
+    if (b + threads < p.B) {  // on their way during this turn's sums
+      next_old = p.old_lens[b + threads];
+      next_new = p.new_lens[b + threads];
     }
     uint32_t rows = min((uint32_t)max(new_len, 0), cap);
 #pragma unroll

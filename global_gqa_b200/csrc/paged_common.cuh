@@ -110,8 +110,7 @@ __device__ __forceinline__ void block_prefix(int n, int* pref, int* warp_sums, F
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int before = inc - sum;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  const int before = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
   for (int i = i0; i < i1; ++i) pref[i + 1] += before;
   if (tid == 0) pref[0] = 0;
   __syncthreads();
