@@ -55,6 +55,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t piece(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// The bits of a bf16 number below x >= 0 (0 for 0) by at least 2^-16 of x's power of two and at most 2^-7 + 2^-16 of it:
+// the rest, which the subtraction gives exactly, is positive wherever x is (above some 2^-110, where bf16 ends), and
+// rounded to bf16 within 2^-16 of x.  Both parts of a weight are then positive, and an infinite V times them is that
+// infinity; with x rounded to nearest the rest can be 0 or negative, which made a NaN of it.
+__device__ __forceinline__ uint32_t high_part(float x) {
+  return (uint32_t)__viaddmax_s32(__float_as_int(x), -0x80, 0) & 0xffff0000u;
+}
+
 // Number of units of one kv head of sequence b (0: nothing to attend to).
 __device__ __forceinline__ int units_of(const PagedDecodeParams& p, int b, bool report) {
   const int L = p.seq_lens[b];
@@ -319,10 +327,10 @@ __global__ void __launch_bounds__(kPagedThreads, D == 64 ? 4 : D == 128 ? 3 : 2)
         // P as the sum of two bf16 numbers, which leaves 2^-16 of each weight: P V then has fp32's precision up to the
         // output's rounding.  One bf16 number alone adds an error as large as that rounding, and saves nothing that
         // can be measured: the second product runs under the loads.
-        const uint32_t ph01 = pack_bf16x2(p0, p1), ph23 = pack_bf16x2(p2, p3);
-        const uint32_t pb0 = transpose8(ph01), pb1 = transpose8(ph23);
-        const uint32_t pl0 = transpose8(pack_bf16x2(p0 - __uint_as_float(ph01 << 16), p1 - __uint_as_float(ph01 & 0xffff0000u)));
-        const uint32_t pl1 = transpose8(pack_bf16x2(p2 - __uint_as_float(ph23 << 16), p3 - __uint_as_float(ph23 & 0xffff0000u)));
+        const uint32_t h0 = high_part(p0), h1 = high_part(p1), h2 = high_part(p2), h3 = high_part(p3);
+        const uint32_t pb0 = transpose8(__byte_perm(h0, h1, 0x7632)), pb1 = transpose8(__byte_perm(h2, h3, 0x7632));
+        const uint32_t pl0 = transpose8(pack_bf16x2(p0 - __uint_as_float(h0), p1 - __uint_as_float(h1)));
+        const uint32_t pl1 = transpose8(pack_bf16x2(p2 - __uint_as_float(h2), p3 - __uint_as_float(h3)));
 #pragma unroll
         for (int j = 0; j < VP; ++j)
 #pragma unroll

@@ -432,7 +432,8 @@ size_t g3attn_paged_decode_workspace_size(int32_t D);
  * recorded) gets a zero row and an lse of -infinity.  A page number out of
  * range, or a list entry that is out of range or not above the one before it,
  * is recorded and left out.  Rows of a page that hold no visible token do not
- * matter, NaN included.
+ * matter, NaN included.  An infinite value in a visible row makes its feature of
+ * the output that infinity (a weight below 2^-100 of the largest may give NaN).
  */
 g3_status g3attn_paged_decode(const void* q_hat, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, const int32_t* seq_lens,

@@ -1,0 +1,50 @@
+"""What the paged calls' documentation promises at the edges of their arguments, one promise per test.
+
+Tolerances are those that test_gpu_paged.py derives."""
+import numpy as np
+import pytest
+import torch
+
+import global_gqa_b200 as g3
+from gpu_helpers import dev
+from test_gpu_paged import clean, decode_case, gi
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,Hkv,G,P", [(64, 2, 2, 16), (128, 2, 3, 32), (256, 1, 4, 16)])
+@pytest.mark.parametrize("lens", [[1, 40, 700], [4097], [9, 33, 1200] + [5, 20] * 400], ids=["few", "one", "many"])
+def test_infinite_values_stay_infinite(D, Hkv, G, P, lens):
+    """An infinity in a visible V row makes its feature that infinity whatever the row's weight, both signs a NaN, and no other feature
+    differs from what it is without them: pairs cut between blocks, whole ones, single warps' ones."""
+    c = decode_case(lens, Hkv * G, Hkv, D, P, 11)
+    call = lambda: g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0,  # noqa: E731
+                                   return_lse=True)
+    plain, plain_lse = call()
+    for b, L in enumerate(lens):
+        for f, t, v in ((3, 0, np.inf), (D // 2, L - 1, -np.inf), (D - 1, L // 2, np.inf)):
+            c["vp"][c["table"][b, t // P], Hkv - 1, t % P, f] = v
+        if L > 1:  # both signs
+            for t, v in ((0, np.inf), (L - 1, -np.inf)):
+                c["vp"][c["table"][b, t // P], Hkv - 1, t % P, 7] = v
+    out, lse = call()
+    hit = out[:, (Hkv - 1) * G:]
+    assert (hit[..., 3] == np.inf).all() and (hit[..., D // 2] == -np.inf).all() and (hit[..., D - 1] == np.inf).all()
+    assert torch.isnan(hit[np.asarray(lens) > 1][..., 7]).all()
+    left = torch.ones_like(out, dtype=torch.bool)
+    left[:, (Hkv - 1) * G:, [3, 7, D // 2, D - 1]] = False
+    assert torch.equal(out[left], plain[left]) and torch.equal(lse, plain_lse) and clean()
+
+
+def test_infinite_values_of_small_weights():
+    """Weights down to 2^-86 of the largest, and one of exactly a power of two."""
+    P, D, L = 16, 64, 40
+    c = decode_case([L], 1, 1, D, P, 3)
+    c["q"][:] = 0
+    c["q"][0, 0, 0] = 64
+    c["kp"][..., 0] = 0
+    for t, k in ((0, -7.5), (20, 0.0), (33, -4.0)):  # exponents 8 k: weights e^-60, 1, e^-32
+        c["kp"][c["table"][0, t // P], 0, t % P, 0] = k
+        c["vp"][c["table"][0, t // P], 0, t % P, t] = np.inf
+    out = g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0)
+    assert (out[0, 0, [0, 20, 33]] == np.inf).all() and int(torch.isfinite(out).sum()) == D - 3 and clean()
