@@ -232,7 +232,8 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     const size_t ws_bytes = g3attn_paged_decode_workspace_size((int32_t)D);
     if (ws_bytes == 0) Py_RETURN_NONE;
-    const bool with_lse = a[8] == Py_True;
+    const int with_lse = PyObject_IsTrue(a[8]);
+    if (with_lse < 0) return nullptr;
     const at::Tensor out = c.empty({B, Hq, D}, kBFloat16), ws = c.empty({(int64_t)ws_bytes}, at::kByte);
     at::Tensor lse;
     if (with_lse) lse = c.empty({B, Hq}, kFloat);

@@ -48,3 +48,14 @@ def test_infinite_values_of_small_weights():
         c["vp"][c["table"][0, t // P], 0, t % P, t] = np.inf
     out = g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0)
     assert (out[0, 0, [0, 20, 33]] == np.inf).all() and int(torch.isfinite(out).sum()) == D - 3 and clean()
+
+
+@pytest.mark.parametrize("flag", [1, np.bool_(True), 0, np.bool_(False), None, True, False])
+def test_lse_is_returned_alike_by_both_ways_of_the_call(flag):
+    c = decode_case([5, 20], 2, 1, 64, 16, 1)
+    args = c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0
+    quick = g3.paged_decode(*args, return_lse=flag)
+    ordinary = g3.paged_decode(*args, return_lse=flag, out=torch.empty_like(args[0]))
+    assert isinstance(quick, tuple) == isinstance(ordinary, tuple) == bool(flag)
+    for a, b in zip(quick, ordinary):
+        assert torch.equal(a, b)
