@@ -425,7 +425,10 @@ size_t g3attn_paged_decode_workspace_size(int32_t D);
  *              is idle
  *   pages      optional int32 [B, Hkv, n_select], GLOBAL layers: attend to these
  *              logical pages only, as page_select gives them (ascending; -1
- *              pads the end).  NULL with n_select = 0: to all
+ *              pads the end).  A list's first ceil(seq_len / page_size) entries
+ *              are read, each compared with the one before it alone: a page
+ *              listed again behind a -1 counts again.  NULL with n_select = 0:
+ *              to all
  *   out        bf16 [B, Hq, D];  lse optional fp32 [B, Hq] (natural log, as prefill's)
  *   workspace  >= g3attn_paged_decode_workspace_size(D) bytes (for any B and lengths)
  * A sequence that sees nothing (idle, or a length out of range, which is

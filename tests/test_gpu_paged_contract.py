@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import global_gqa_b200 as g3
+from oracle import paged as PG
 from gpu_helpers import dev
-from test_gpu_paged import clean, decode_case, gi
+from test_gpu_paged import clean, decode_case, gi, near_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -48,6 +49,22 @@ def test_infinite_values_of_small_weights():
         c["vp"][c["table"][0, t // P], 0, t % P, t] = np.inf
     out = g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0)
     assert (out[0, 0, [0, 20, 33]] == np.inf).all() and int(torch.isfinite(out).sum()) == D - 3 and clean()
+
+
+def test_list_entries_behind_a_pad():
+    """An entry is compared with the one before it alone: pages behind a -1 are attended to, one listed again counts again; entries behind
+    the sequence's number of pages are not read."""
+    L, P, D = 96, 16, 64
+    c = decode_case([L, L, 2 * P], 2, 1, D, P, 5)
+    listed = np.array([[[5, -1, 5, -1]], [[0, -1, 4, -1]], [[0, 1, 0, 9]]])
+    ref = PG.paged_decode(c["q"], c["kp"].double().numpy(), c["vp"].double().numpy(), c["table"], c["lens"], 1, 0, listed[:, :, :3] * 1)
+    one = PG.paged_decode(c["q"][2:], c["kp"].double().numpy(), c["vp"].double().numpy(), c["table"][2:], c["lens"][2:], 1, 0)
+    for r, o in zip(ref, one):
+        r[2] = o[0]
+    out, lse = g3.paged_decode(c["q"].to(dev()), c["kp"].to(dev()), c["vp"].to(dev()), gi(c["table"]), gi(c["lens"]), g3.GLOBAL, 0,
+                               pages=gi(listed), return_lse=True)
+    near_decode(out, lse, ref, D, L)
+    assert clean()
 
 
 @pytest.mark.parametrize("flag", [1, np.bool_(True), 0, np.bool_(False), None, True, False])
