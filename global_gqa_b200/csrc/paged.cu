@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kBoundsThreads, 4) page_bounds_kernel(PageBoun
       if (blockIdx.x == 0) record_error(p.status, kErrInvalid, 320);
       return 0;
     }
-    return max(0, ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift));
+    return old < L ? ((L + (1 << p.page_shift) - 1) >> p.page_shift) - (old >> p.page_shift) : 0;
   });
   const int units = bounds_smem[p.B] * p.Hkv;  // below 2^30: checked on the host for the widest table
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LPT, sub = lane / LPT;

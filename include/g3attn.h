@@ -374,7 +374,8 @@ g3_status g3attn_paged_append(const void* q, const void* k, const void* v,
  *
  *   old_lens, seq_lens int32 [B]  the pages that hold tokens old .. seq_len-1
  *              are renewed from all their rows below seq_len (a page that is
- *              filled up by one step is renewed as a whole)
+ *              filled up by one step is renewed as a whole); none where
+ *              old >= seq_len
  *   bounds     int8 [n_pages, Hkv, 2, D]: min(127, ceil(largest * 2^e)), then
  *              max(-127, floor(smallest * 2^e))
  *   exps       int8 [n_pages, Hkv]: e, the largest with max|key| * 2^e <= 127,

@@ -76,3 +76,20 @@ def test_lse_is_returned_alike_by_both_ways_of_the_call(flag):
     assert isinstance(quick, tuple) == isinstance(ordinary, tuple) == bool(flag)
     for a, b in zip(quick, ordinary):
         assert torch.equal(a, b)
+
+
+def test_no_new_tokens_renew_no_bounds():
+    """old == seq_len, or above it, inside a page and at its border: nothing is read, written or recorded."""
+    P, D = 16, 64
+    k = torch.randn(8, 2, P, D, generator=torch.Generator().manual_seed(2)).bfloat16().to(dev())
+    bounds, exps = torch.full((8, 2, 2, D), 99, dtype=torch.int8, device=dev()), torch.full((8, 2), 99, dtype=torch.int8, device=dev())
+    old, lens = [5, 20, 30, 16, 20, 31, 0, 32], [5, 20, 20, 16, 3, 17, 0, 32]
+    for page in (-1, 0, 8):  # also where the table holds no page
+        g3.page_bounds(k, gi(np.full((8, 2), page)), gi(old), gi(lens), bounds, exps)
+        assert clean() and (bounds == 99).all() and (exps == 99).all()
+    table = np.arange(8).reshape(4, 2)
+    g3.page_bounds(k, gi(table), gi([5, 20, 7, 32]), gi([5, 21, 7, 32]), bounds, exps)  # one of four has a token
+    assert clean() and (bounds[[0, 1, 2, 4, 5, 6, 7]] == 99).all()
+    for h in range(2):
+        ref, e = PG.page_bounds_of(k[3, h, :5].cpu())
+        assert bounds[3, h].cpu().tolist() == ref.tolist() and int(exps[3, h]) == e
