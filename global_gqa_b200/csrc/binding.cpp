@@ -105,17 +105,22 @@ PyObject* page_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t P = c.number(a[5]), n_pages = c.number(a[6]), T = c.number(a[7]);
     int32_t* status = c.status(a[8]);
     if (!c.ok || T < 1 || B > INT32_MAX || pages > INT32_MAX || cap > INT32_MAX) Py_RETURN_NONE;
-    // One allocation: five tensors that share its storage, each on a 256-byte boundary.
+    // One allocation of tensors that share its storage, on 256-byte boundaries; a second one (0.6 of 6 us of host time)
+    // for the token rows where there are many, so that kept lengths do not keep a prompt's rows alive.
     const int64_t sizes[5] = {B, B + 1, T, T, 2};
-    int64_t at = 0, begin[5];
+    const int apart = T > 8192 ? 1 : 0;
+    const int in[5] = {0, 0, apart, apart, 0};
+    int64_t total[2] = {0, 0}, begin[5];
     for (int i = 0; i < 5; ++i) {
-      begin[i] = at;
-      at += (sizes[i] + 63) / 64 * 64;
+      begin[i] = total[in[i]];
+      total[in[i]] += (sizes[i] + 63) / 64 * 64;
     }
-    const at::Tensor all = c.empty({at}, kInt);
+    at::Tensor all[2];
+    for (int k = 0; k <= apart; ++k) all[k] = c.empty({total[k]}, kInt);
     at::Tensor out[5];
     for (int i = 0; i < 5; ++i) {
-      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      const at::Tensor& t = all[in[i]];
+      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
       out[i].unsafeGetTensorImpl()->set_storage_offset(begin[i]);
       out[i].unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&sizes[i], 1));
     }

@@ -93,3 +93,16 @@ def test_no_new_tokens_renew_no_bounds():
     for h in range(2):
         ref, e = PG.page_bounds_of(k[3, h, :5].cpu())
         assert bounds[3, h].cpu().tolist() == ref.tolist() and int(exps[3, h]) == e
+
+
+@pytest.mark.parametrize("T", [4, 8192, 8193, 100000])
+def test_kept_lengths_hold_few_token_rows(T):
+    """What a server keeps from step to step does not keep a prompt's slots and positions alive: 64 KB of them at most."""
+    B = 4
+    got = g3.page_map(gi([0] * B), gi([1] * B), gi(np.full((B, 2), -1)), gi(np.arange(9)), gi([0, 9]), 16, 9, T)
+    for k in ("seq_lens", "cu_tokens", "free_state"):
+        assert got[k].untyped_storage().nbytes() <= 2 * 4 * 8192 + 4096
+    places = sorted((got[k].data_ptr(), got[k].data_ptr() + got[k].numel() * 4) for k in got)
+    assert all(a[1] <= b[0] and b[0] % 256 == 0 for a, b in zip(places, places[1:]))
+    assert got["seq_lens"].tolist() == [1] * B and got["cu_tokens"].tolist() == [0, 1, 2, 3, 4] and got["free_state"].tolist() == [4, 5]
+    assert got["slots"][:4].tolist() == [0, 16, 32, 48] and (got["slots"][4:] == -1).all() and (got["positions"] == 0).all() and clean()
