@@ -1,5 +1,6 @@
-"""Builds libg3attn.so (the C-ABI library) in-tree with nvcc for sm_100a, and
-_paged.so, the Python module that calls its paged-cache part.
+"""Builds libg3attn.so (the C-ABI library) in-tree with nvcc for sm_100a, and,
+where torch is installed, _paged.so, the Python module that calls its
+paged-cache part.
 
 Usage: python -m global_gqa_b200.build  [--force] [--verbose]
 """
@@ -91,11 +92,15 @@ def build_fault_inject(force: bool = False) -> str:
 BINDING = os.path.join(HERE, "_paged.so")
 
 
-def build_binding(force: bool = False) -> str:
-    """The module that calls the library's paged-cache part from Python (csrc/binding.cpp), for this torch."""
+def build_binding(force: bool = False) -> "str | None":
+    """The module that calls the library's paged-cache part from Python (csrc/binding.cpp), for this torch; None without torch."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        sys.stderr.write("torch is not installed: _paged.so is not built (the library is complete without it)\n")
+        return None
     src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "g3attn.h")
     base = os.path.dirname(torch.__file__)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

@@ -9,6 +9,7 @@ import global_gqa_b200 as g3
 from oracle import paged as PG
 from gpu_helpers import dev
 from test_gpu_paged import clean, decode_case, gi, near_decode
+from test_gpu_paged_serving import Step, same
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +107,19 @@ def test_kept_lengths_hold_few_token_rows(T):
     assert all(a[1] <= b[0] and b[0] % 256 == 0 for a, b in zip(places, places[1:]))
     assert got["seq_lens"].tolist() == [1] * B and got["cu_tokens"].tolist() == [0, 1, 2, 3, 4] and got["free_state"].tolist() == [4, 5]
     assert got["slots"][:4].tolist() == [0, 16, 32, 48] and (got["slots"][4:] == -1).all() and (got["positions"] == 0).all() and clean()
+
+
+def test_a_step_runs_alike_without_the_quick_module(monkeypatch):
+    """The calls of a box that built the C library alone: the ordinary way, the same bits."""
+    a, b = Step(7), Step(7)
+    for _ in range(3):
+        a.run()
+    monkeypatch.setattr(g3, "_quick", None)
+    monkeypatch.setattr(g3, "HERE", "/nonexistent")
+    with pytest.warns(RuntimeWarning, match="_paged.so is missing"):
+        b.run()
+    for _ in range(2):
+        b.run()
+    torch.cuda.synchronize()
+    same(a, b)
+    assert clean() and g3._quick is g3._Ordinary
