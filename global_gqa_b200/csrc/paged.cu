@@ -883,12 +883,17 @@ template <int D, int THREADS>
 static cudaError_t launch_select_d(PageSelectParams p, cudaStream_t st) {
   const long long pairs = (long long)p.B * p.Hkv;
   constexpr int WARPS = THREADS / 32;
-  // Blocks per pair: up to 8, at least 16 pages for each of their warps, no more than find a place at once.
+  // Blocks per pair: up to 8, at least 16 pages for each of their warps, no more than find a place at once (2 per SM at
+  // D = 256, else 4).  A second wave sets up and joins its clusters again: 200 pairs of D = 256 take 12.7 us in one wave
+  // of single blocks against 18.3 with two blocks per pair for up to 512 pages, 34.7 against 34.9 for 2048, 250 pairs
+  // 14.0 against 21.4 and 37.6 against 40.9; only around 160 pairs of 2048 pages is the second wave shorter (27.6
+  // against 33.1).
   int ranks = 1;
-  while (ranks < 8 && ranks * WARPS * 16 < p.max_pages && pairs * ranks < 148 * 2) ranks *= 2;
+  constexpr int kPlaces = 148 * (D == 256 ? 2 : 4);
+  while (ranks < 8 && ranks * WARPS * 16 < p.max_pages && pairs * ranks * 2 <= kPlaces) ranks *= 2;
   // More blocks than find a place at once: the long sequences first (56 us against 61 for 1024 pairs of up to
   // 2048 pages), as far as a block can rank them with a thread each.
-  p.by_length = pairs * ranks > 148 * (D == 256 ? 2 : 4) && p.B <= THREADS;
+  p.by_length = pairs * ranks > kPlaces && p.B <= THREADS;
   // Room for the scores of the longest table, up to 32 KB: 8192 pages in a single sequence took 22 us so and 33 with
   // their scores in L2 (blocks of 256), while 32 KB for every call cost the short ones 0.4 us and the batch above 4.
   p.keys_in_smem = std::min(p.max_pages, kKeysInSmem);

@@ -8,7 +8,7 @@ import torch
 import global_gqa_b200 as g3
 from oracle import paged as PG
 from gpu_helpers import dev
-from test_gpu_paged import clean, decode_case, gi, near_decode
+from test_gpu_paged import check_select, clean, decode_case, gi, near_decode
 from test_gpu_paged_serving import Step, same
 
 pytestmark = pytest.mark.gpu
@@ -94,6 +94,32 @@ def test_no_new_tokens_renew_no_bounds():
     for h in range(2):
         ref, e = PG.page_bounds_of(k[3, h, :5].cpu())
         assert bounds[3, h].cpu().tolist() == ref.tolist() and int(exps[3, h]) == e
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B", [2, 24])
+def test_page_select_of_more_pages_than_fit_on_chip(D, B):
+    """Block tables above 8192 pages, scores in the workspace: few pairs (blocks of 512 threads) and more (of 256)."""
+    P, n, n_pages = 16, 100, 700
+    rng, g = np.random.default_rng(B + D), torch.Generator().manual_seed(B + D)
+    lens = rng.integers(100 * P, 8193 * P, B)
+    lens[0], lens[-1] = 8500 * P - 3, 8193 * P
+    table = rng.integers(0, n_pages, (B, 8500))
+    bounds = torch.randint(-127, 128, (n_pages, 1, 2, D), generator=g).to(torch.int8)
+    exps = torch.randint(2, 5, (n_pages, 1), generator=g).to(torch.int8)
+    check_select(torch.randn(B, 3, D, generator=g).bfloat16(), bounds, exps, table, lens, P, n)  # pages repeat: many ties
+    assert clean()
+
+
+@pytest.mark.parametrize("D,B", [(256, 150), (256, 295), (128, 296), (256, 148), (64, 148), (256, 74)])
+def test_page_select_pairs_around_the_clusters_limits(D, B):
+    P, n, n_pages = 16, 9, 700
+    rng, g = np.random.default_rng(B + D), torch.Generator().manual_seed(B + D)
+    lens = rng.integers(0, 600 * P, B)
+    table = rng.integers(0, n_pages, (B, 600))
+    bounds = torch.randint(-127, 128, (n_pages, 1, 2, D), generator=g).to(torch.int8)
+    check_select(torch.randn(B, 2, D, generator=g).bfloat16(), bounds, torch.full((n_pages, 1), 4, dtype=torch.int8), table, lens, P, n)
+    assert clean()
 
 
 @pytest.mark.parametrize("T", [4, 8192, 8193, 100000])
