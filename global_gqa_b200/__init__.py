@@ -633,7 +633,11 @@ def paged_append(k, v, k_gamma, positions, slots, k_pages, v_pages, rope_base: f
 
     k, v bf16 [T,Hkv,D] and q bf16 [T,Hq,D] raw projections, gammas fp32 [D],
     positions and slots int32 [T] (slot below 0: not cached), k_pages/v_pages bf16
-    [n_pages,Hkv,page_size,D] (updated in place).
+    [n_pages,Hkv,page_size,D] (updated in place).  Rows are packed as page_map's
+    cu_tokens says, none for a sequence that waits: row b of what page_select and
+    paged_decode take is
+    q_hat.index_select(0, (cu_tokens[1:] - 1).clamp(min=0)), which is q_hat
+    itself only where every sequence has one new token.
     """
     if q_hat is None and stream is None:
         r = (_quick or _load_quick()).paged_append(k, v, k_gamma, positions, slots, k_pages, v_pages, rope_base, interp_factor,
@@ -687,7 +691,8 @@ def page_select(q_hat, bounds, exps, block_table, seq_lens, page_size: int, n_se
                 status=None, stream=None):
     """The newest page and the n_select-1 best-scored others of each (sequence, kv head), ascending, -1 behind.
 
-    q_hat bf16 [B,Hq,D] from paged_append, bounds/exps from page_bounds; returns
+    q_hat bf16 [B,Hq,D], row b for sequence b (see paged_append), bounds/exps from
+    page_bounds; returns
     int32 [B,Hkv,n_select], for paged_decode(pages=...).
     """
     if out is None and ws is None and stream is None:
@@ -717,8 +722,8 @@ def paged_decode(q_hat, k_pages, v_pages, block_table, seq_lens, layer_kind: int
                  return_lse: bool = False, ws=None, status=None, stream=None):
     """Attention of one new token per sequence over its pages; returns out [B,Hq,D] (and lse [B,Hq]).
 
-    q_hat bf16 [B,Hq,D] from paged_append, k_pages/v_pages bf16
-    [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages], seq_lens int32 [B]
+    q_hat bf16 [B,Hq,D], row b for sequence b (see paged_append), k_pages/v_pages
+    bf16 [n_pages,Hkv,page_size,D], block_table int32 [B,max_pages], seq_lens int32 [B]
     (the new token included; 0: idle, a zero row), pages int32 [B,Hkv,n] from
     page_select or None (all pages; the last `window` tokens on a LOCAL layer).
     """

@@ -309,6 +309,12 @@ g3_status g3attn_decode_no_alloc(const void* q, const void* k_new, const void* v
  * The calls are ordered by their stream alone and may be captured in a graph.
  * A serving step is: page_map once for all layers, then per layer paged_append,
  * (page_bounds and page_select on a sparse global layer,) paged_decode.
+ * paged_append's rows are packed: a sequence that waits a step has none.
+ * page_select and paged_decode have a row for every sequence: row b of their
+ * q_hat is the packed row cu_tokens[b + 1] - 1, its newest token's.  Only where
+ * every sequence has exactly one new token are the two the same; otherwise
+ * gather the rows first (any row for a sequence that waits, whose output row
+ * then means nothing).
  */
 
 /*
@@ -402,7 +408,8 @@ size_t g3attn_page_select_workspace_size(int32_t B, int32_t Hkv, int32_t max_pag
  * rounding of q.  Equal scores: the lower page.  Whole-number sums, so the
  * result does not depend on their order.
  *
- *   q_hat      bf16 [B, Hq, D] from paged_append (a NaN feature counts as 0)
+ *   q_hat      bf16 [B, Hq, D] row b the query of sequence b, from paged_append's
+ *              packed rows (see above; a NaN feature counts as 0)
  *   seq_lens   int32 [B] tokens cached, the new one included
  *   pages      int32 [B, Hkv, n_select]  logical pages, ascending; -1 behind the
  *              last one where a sequence has fewer
@@ -420,7 +427,8 @@ size_t g3attn_paged_decode_workspace_size(int32_t D);
 /*
  * Attention of one new token per sequence over its pages (steps 3 and 4 above).
  *
- *   q_hat      bf16 [B, Hq, D] from paged_append
+ *   q_hat      bf16 [B, Hq, D] row b the query of sequence b, from paged_append's
+ *              packed rows (see above)
  *   seq_lens   int32 [B] tokens cached, the new one included: a GLOBAL layer
  *              sees all of them, a LOCAL one the last `window`.  0: the sequence
  *              is idle

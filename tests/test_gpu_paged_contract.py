@@ -6,14 +6,17 @@ import pytest
 import torch
 
 import global_gqa_b200 as g3
+import inputs
 from oracle import paged as PG
 from gpu_helpers import dev
-from test_gpu_paged import check_select, clean, decode_case, gi, near_decode
-from test_gpu_paged_serving import Step, same
+from test_gpu_paged import check_select, clean, decode_case, gi, near_decode, reported, scattered
+from test_gpu_paged_serving import Pool, Step, layer, near, same
 
 pytestmark = pytest.mark.gpu
+i32 = torch.int32
 
 
+# ------------------------------------------------------------------ decode
 @pytest.mark.parametrize("D,Hkv,G,P", [(64, 2, 2, 16), (128, 2, 3, 32), (256, 1, 4, 16)])
 @pytest.mark.parametrize("lens", [[1, 40, 700], [4097], [9, 33, 1200] + [5, 20] * 400], ids=["few", "one", "many"])
 def test_infinite_values_stay_infinite(D, Hkv, G, P, lens):
@@ -79,6 +82,7 @@ def test_lse_is_returned_alike_by_both_ways_of_the_call(flag):
         assert torch.equal(a, b)
 
 
+# ------------------------------------------------------------------ bounds
 def test_no_new_tokens_renew_no_bounds():
     """old == seq_len, or above it, inside a page and at its border: nothing is read, written or recorded."""
     P, D = 16, 64
@@ -96,6 +100,7 @@ def test_no_new_tokens_renew_no_bounds():
         assert bounds[3, h].cpu().tolist() == ref.tolist() and int(exps[3, h]) == e
 
 
+# ------------------------------------------------------------------ select
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("B", [2, 24])
 def test_page_select_of_more_pages_than_fit_on_chip(D, B):
@@ -122,6 +127,7 @@ def test_page_select_pairs_around_the_clusters_limits(D, B):
     assert clean()
 
 
+# --------------------------------------------------------------------- map
 @pytest.mark.parametrize("T", [4, 8192, 8193, 100000])
 def test_kept_lengths_hold_few_token_rows(T):
     """What a server keeps from step to step does not keep a prompt's slots and positions alive: 64 KB of them at most."""
@@ -133,6 +139,110 @@ def test_kept_lengths_hold_few_token_rows(T):
     assert all(a[1] <= b[0] and b[0] % 256 == 0 for a, b in zip(places, places[1:]))
     assert got["seq_lens"].tolist() == [1] * B and got["cu_tokens"].tolist() == [0, 1, 2, 3, 4] and got["free_state"].tolist() == [4, 5]
     assert got["slots"][:4].tolist() == [0, 16, 32, 48] and (got["slots"][4:] == -1).all() and (got["positions"] == 0).all() and clean()
+
+
+# ----------------------------------------------------------------- serving
+def newest_rows(q_hat, cu_tokens):
+    """The packed rows of each sequence's newest token, as the documentation gathers them."""
+    return q_hat.index_select(0, (cu_tokens[1:] - 1).clamp(min=0))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,P", [(4, 2, 64, 16), (8, 2, 128, 32), (4, 1, 256, 16)])
+def test_sequences_with_a_history_wait_a_step(Hq, Hkv, D, P):
+    """Steps in which some sequences get no token: the others' results are those of the contiguous decode, and what
+    belongs to a waiting one (table, length, pages, bounds) is left as it was."""
+    B, W, cap, n_pages = 4, 48, 200, 60
+    pool = Pool(2, n_pages, B, -(-cap // P), Hkv, D, P)
+    ring = [[torch.zeros(B, Hkv, W if li == 0 else cap, D, dtype=torch.bfloat16, device=dev()) for _ in "kv"] for li in range(2)]
+    gains = [inputs.prefill_layer_inputs(1, 1, Hq, Hkv, D, seed=0, layer=li) for li in range(2)]
+    gains = [(x["q_gamma"].to(dev()), x["k_gamma"].to(dev())) for x in gains]
+    prompts = [70, 31, 50, 33]
+    got = pool.map(prompts, sum(prompts))
+    for li in range(2):
+        kind, win, base, interp = layer(li, W)
+        packed = [torch.empty(sum(prompts), Hkv, D, dtype=torch.bfloat16, device=dev()) for _ in "kv"]
+        for b, n in enumerate(prompts):
+            x = {k: v.to(dev()) for k, v in inputs.prefill_layer_inputs(1, n, Hq, Hkv, D, seed=60 + b, layer=li).items() if v is not None}
+            kc, vc = ring[li][0][b:b + 1], ring[li][1][b:b + 1]
+            g3.prefill(x["q"], x["k"], x["v"], *gains[li], x["positions"], kind, win, base, interp, k_cache=kc, v_cache=vc)
+            r0 = int(got["cu_tokens"][b])
+            packed[0][r0:r0 + n], packed[1][r0:r0 + n] = x["k"][0], x["v"][0]
+        g3.paged_append(*packed, gains[li][1], got["positions"], got["slots"], pool.k[li], pool.v[li], base, interp)
+    g3.page_bounds(pool.k[1], pool.table, pool.old, pool.lens, pool.bounds, pool.exps)
+
+    for s, active in enumerate([[1, 0, 1, 1], [0, 1, 1, 1], [1, 1, 1, 0], [0, 0, 1, 0], [1, 0, 0, 1], [0, 0, 0, 0], [1, 1, 1, 1]] * 3):
+        rows, waiting = [b for b in range(B) if active[b]], [b for b in range(B) if not active[b]]
+        before = pool.table.clone(), pool.lens.clone(), pool.bounds.clone(), pool.exps.clone(), [k.clone() for k in pool.k + pool.v]
+        theirs = torch.cat([pool.table[b, :-(-int(pool.lens[b]) // P)] for b in waiting]).long() if waiting else torch.empty(0, dtype=torch.long)
+        got = pool.map(active, B)
+        for li in range(2):
+            kind, win, base, interp = layer(li, W)
+            x = {k: v.to(dev()) for k, v in inputs.decode_step_inputs(B, Hq, Hkv, D, seed=80 + s, layer=li).items()}
+            packed = {k: torch.full_like(x[k], float("nan")) for k in ("q", "k_new", "v_new")}
+            for k in packed:
+                packed[k][:len(rows)] = x[k][rows]
+            q_hat = g3.paged_append(packed["k_new"], packed["v_new"], gains[li][1], got["positions"], got["slots"], pool.k[li], pool.v[li],
+                                    base, interp, q=packed["q"], q_gamma=gains[li][0])
+            q_seq = newest_rows(q_hat, got["cu_tokens"])
+            out, lse = g3.paged_decode(q_seq, pool.k[li], pool.v[li], pool.table, pool.lens, kind, win, return_lse=True)
+            kept = [[c[waiting].clone() for c in pair] for pair in ring]
+            lens = pool.lens.tolist()
+            ref = g3.decode(x["q"], x["k_new"], x["v_new"], *gains[li], *ring[li], gi(lens), cap, kind, win, base, interp)
+            for pair, old in zip(ring, kept):  # the contiguous call steps every sequence
+                for c, o in zip(pair, old):
+                    c[waiting] = o
+            if rows:
+                near(out[rows], ref[rows])
+            if li == 1:
+                g3.page_bounds(pool.k[1], pool.table, pool.old, pool.lens, pool.bounds, pool.exps)
+                some = g3.page_select(q_seq, pool.bounds, pool.exps, pool.table, pool.lens, P, 2)
+                part = g3.paged_decode(q_seq, pool.k[1], pool.v[1], pool.table, pool.lens, kind, win, pages=some)
+                kp, vp = torch.nan_to_num(pool.k[1]).double().cpu().numpy(), torch.nan_to_num(pool.v[1]).double().cpu().numpy()
+                if rows:
+                    r = PG.paged_decode(q_seq[rows].cpu(), kp, vp, pool.table[rows].cpu(), pool.lens[rows].tolist(), 1, win, some[rows].cpu().numpy())
+                    near(part[rows], torch.from_numpy(r[0]).to(dev()))
+        assert torch.equal(pool.table[waiting], before[0][waiting]) and torch.equal(pool.lens[waiting], before[1][waiting])
+        assert torch.equal(pool.bounds[theirs], before[2][theirs]) and torch.equal(pool.exps[theirs], before[3][theirs])
+        for now, was in zip(pool.k + pool.v, before[4]):
+            assert torch.equal(now[theirs].view(torch.int16), was[theirs].view(torch.int16))
+        assert clean()
+
+
+def test_captured_steps_with_waiting_sequences():
+    """One captured step serves every choice of sequences that wait: the gather of the rows is in the graph."""
+    def step(s):
+        p = s.pool
+        got = g3.page_map(p.lens, s.one, p.table, p.ring, p.state, p.P, p.n_pages, len(s.one))
+        q_hat = g3.paged_append(s.k, s.v, s.gain, got["positions"], got["slots"], p.k[0], p.v[0], 1e6, 8.0, q=s.q, q_gamma=s.gain)
+        g3.page_bounds(p.k[0], p.table, p.lens, got["seq_lens"], p.bounds, p.exps)
+        q_seq = newest_rows(q_hat, got["cu_tokens"])
+        pages = g3.page_select(q_seq, p.bounds, p.exps, p.table, got["seq_lens"], p.P, s.n)
+        out, lse = g3.paged_decode(q_seq, p.k[0], p.v[0], p.table, got["seq_lens"], g3.GLOBAL, 0, pages=pages, return_lse=True)
+        for into, new in ((s.out, out), (s.seen, lse), (p.lens, got["seq_lens"]), (p.state, got["free_state"])):
+            into.copy_(new)
+        return q_hat
+
+    g3.paged_status(dev())
+    eager, captured = Step(8), Step(8)
+    for s in (eager, captured):
+        step(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(captured)
+    for active in ([1, 0, 1, 1, 0], [0, 0, 0, 0, 1], [1, 1, 1, 1, 1], [0, 0, 0, 0, 0], [0, 1, 0, 1, 0]) * 4:
+        for s in (eager, captured):
+            s.one.copy_(gi(active))
+        q_hat, rows = step(eager), [b for b in range(5) if active[b]]
+        graph.replay()
+        torch.cuda.synchronize()
+        same(eager, captured)
+        if rows:  # each running sequence's output is the attention of its own packed row
+            p, q = eager.pool, q_hat[:len(rows)].contiguous()
+            table, lens = p.table[rows].contiguous(), p.lens[rows].contiguous()
+            pages = g3.page_select(q, p.bounds, p.exps, table, lens, p.P, eager.n)
+            near(eager.out[rows], g3.paged_decode(q, p.k[0], p.v[0], table, lens, g3.GLOBAL, 0, pages=pages))
+    assert clean()
 
 
 def test_a_step_runs_alike_without_the_quick_module(monkeypatch):
