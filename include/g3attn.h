@@ -329,7 +329,8 @@ g3_status g3attn_decode_no_alloc(const void* q, const void* k_new, const void* v
  *              the order of the sequences.  To give pages back, write them
  *              behind the last one ((head + count) % free_capacity) and raise count
  *   max_tokens rows of slots and positions, at most 2^30
- *   seq_lens   int32 [B]  old + new, or old where the sequence was refused
+ *   seq_lens   int32 [B]  old + new, or old where the sequence was refused (0
+ *              where old itself is negative or past the table)
  *   cu_tokens  int32 [B + 1]  first row of each sequence's new tokens in the
  *              packed order of the sequences (refused ones keep their rows)
  *   slots, positions int32 [max_tokens]  of each packed row; -1 and 0 for
