@@ -1001,6 +1001,7 @@ g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8
                              size_t workspace_bytes, int32_t* status, void* stream) {
   g_last_error.clear();
   if (n_select < 1) return fail(G3_ERR_INVALID_ARG, "page_select: n_select=%d", n_select);
+  if (n_select > 1 << 30) return fail(G3_ERR_UNSUPPORTED, "page_select: n_select %d, at most 2^30 are built", n_select);
   if (!q_hat || !bounds || !exps || !block_table || !seq_lens || !pages)
     return fail(G3_ERR_INVALID_ARG, "page_select: a required pointer is NULL");
   if ((long long)B * Hkv > 0x7fffffffLL / 8) return fail(G3_ERR_UNSUPPORTED, "page_select: %d x %d pairs are too many", B, Hkv);

@@ -413,7 +413,7 @@ size_t g3attn_page_select_workspace_size(int32_t B, int32_t Hkv, int32_t max_pag
  *              packed rows (see above; a NaN feature counts as 0)
  *   seq_lens   int32 [B] tokens cached, the new one included
  *   pages      int32 [B, Hkv, n_select]  logical pages, ascending; -1 behind the
- *              last one where a sequence has fewer
+ *              last one where a sequence has fewer; n_select at most 2^30
  *   workspace  >= g3attn_page_select_workspace_size(B, Hkv, max_pages) bytes
  */
 g3_status g3attn_page_select(const void* q_hat, const int8_t* bounds, const int8_t* exps,
