@@ -488,9 +488,9 @@ def _load_quick():
             from . import _paged
             _quick = _paged
         else:
-            warnings.warn("_paged.so is missing: each paged call takes 10 to 20 us of host time instead of 3 to 8 "
+            _quick = _Ordinary  # first: where warnings are errors, the next call goes on
+            warnings.warn("_paged.so is missing: each paged call takes 11 to 23 us of host time instead of 3 to 8 "
                           "(build it with `python -m global_gqa_b200.build`)", RuntimeWarning, stacklevel=3)
-            _quick = _Ordinary
     return _quick
 
 

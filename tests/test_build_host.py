@@ -41,3 +41,18 @@ def test_paged_calls_without_the_quick_module_take_the_ordinary_way(monkeypatch)
     with pytest.raises(ValueError, match="CUDA"):
         g3.page_bounds(torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16), i32[:, None], i32, i32, None, None)
     assert g3._quick is g3._Ordinary  # and says so once
+
+
+def test_a_warning_that_is_an_error_stops_one_call_only(monkeypatch):
+    import warnings
+
+    import torch
+    monkeypatch.setattr(g3, "_quick", None)
+    monkeypatch.setattr(g3, "HERE", os.path.join(g3.ROOT, "nonexistent"))
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning):
+            g3.page_map(i32, i32, i32[:, None], i32, i32, 16, 4, 8)
+        with pytest.raises(ValueError, match="CUDA"):
+            g3.page_map(i32, i32, i32[:, None], i32, i32, 16, 4, 8)
